@@ -325,6 +325,65 @@ int eagle_forward_launches(int64_t B, int64_t T, int64_t C);
 wkv_status eagle_decode_step(int64_t N, int64_t L, int64_t C, const float* w, const float* r, const float* k,
                              const float* v, float* state_inout, float* y, cudaStream_t stream);
 
+/*
+ * Gated linear recurrence: a per-channel recurrence whose decay depends on the token, where
+ * RWKV-4 and Eagle above have one decay per channel (the pages stop at naming such decays; the
+ * formula here is the common one whose input weight is what the gate forgets).  Per sequence b
+ * and channel c, sigma the logistic function:
+ *
+ *   f_t = sigma(g_t),   h_t = f_t h_{t-1} + (1 - f_t) x_t,   y_t = h_t
+ *
+ * g is the gate's logit: g = +inf keeps the state to its rounding whatever the finite x (a
+ * padding token), g = -inf replaces it (h_t = x_t exactly: a document boundary).  A state buffer is
+ * [rows][C] fp32, the empty state zeros.  Arithmetic is fp32 for both I/O types.  A NaN gate,
+ * or a non-finite x or state, makes the later outputs of its sequence and channel non-finite
+ * and touches no other channel.
+ *
+ * gated_scan_forward: prefill over [B, T, C].
+ *   g, x       [B, T, C] in dtype io
+ *   state_in   [B][C] fp32, or NULL for the empty state
+ *   y          [B, T, C] in dtype io (written; must not overlap the inputs)
+ *   state_out  [B][C] fp32, the state after the last token, or NULL (may be state_in)
+ *   carry      gated_scan_carry_size() bytes (written), or NULL: [B][ceil(T / 128)][C] fp32,
+ *              the state entering each 128 steps, which gated_scan_backward reads
+ * T = 0 writes state_out only (state_in, or zeros).  One launch without a workspace; the sums
+ * are taken in a fixed order, so equal calls give equal bits.
+ * Status codes as wkv_forward; WKV_ERR_UNSUPPORTED when B * ceil(C / 32) exceeds 2^28 - 1 (one
+ * launch's blocks).
+ */
+wkv_status gated_scan_forward(int64_t B, int64_t T, int64_t C, wkv_dtype io, const void* g, const void* x,
+                              const float* state_in, void* y, float* state_out, float* carry, cudaStream_t stream);
+
+/* Bytes of the forward's `carry`: 4 per sequence, channel and 128 steps (rounded up). */
+size_t gated_scan_carry_size(int64_t B, int64_t T, int64_t C);
+
+/*
+ * Backward of gated_scan_forward: for a loss L of y and of the final state, with gy = dL/dy and
+ * gs = dL/dstate_out, h_{-1} = state_in and lam_t = dL/dh_t over all paths:
+ *   lam_t = gy_t + f_{t+1} lam_{t+1},  lam_{T-1} = gy_{T-1} + gs
+ *   gg_t = dL/dg_t = f_t (1 - f_t) (h_{t-1} - x_t) lam_t,   gx_t = dL/dx_t = (1 - f_t) lam_t
+ *   gstate_in = dL/dstate_in = f_0 lam_0
+ *   g, x, gy    [B, T, C] in dtype io
+ *   carry       as gated_scan_forward wrote it for the same g, x and state_in
+ *   gstate_out  [B][C] fp32 (gs), or NULL for zeros
+ *   gg, gx      [B, T, C] in dtype io (written; must not overlap the inputs or each other)
+ *   gstate_in   [B][C] fp32 (written, may be gstate_out), or NULL
+ * T = 0 writes gstate_in only (gstate_out, or zeros).  g, x, gy are read once; one launch, no
+ * workspace, no atomics (equal calls give equal bits).  Status codes as gated_scan_forward.
+ */
+wkv_status gated_scan_backward(int64_t B, int64_t T, int64_t C, wkv_dtype io, const void* g, const void* x,
+                               const float* carry, const void* gy, const float* gstate_out, void* gg, void* gx,
+                               float* gstate_in, cudaStream_t stream);
+
+/*
+ * One token of the gated linear recurrence for N sessions x L layers x C channels.
+ *   g, x, y      [N][L][C] in dtype io (y written; must not overlap the inputs)
+ *   state_inout  [N][L][C] fp32, updated in place
+ * With L = 1 and N = B, state_out of gated_scan_forward continues the same sequences.
+ */
+wkv_status gated_scan_step(int64_t N, int64_t L, int64_t C, wkv_dtype io, const void* g, const void* x,
+                           float* state_inout, void* y, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* wkv_status_string(wkv_status status);
 

@@ -16,6 +16,10 @@ Entry points (same names as the C ABI):
 * ``wkv_decode_step_fused(mu, w, u, x_t, x_prev, k, v, state, xbar=None, y=None)``
   -> ``(xbar, y)``.
 * ``token_shift_mix(mu, x, x_last=None)`` -> ``xbar``.
+* ``gated_scan_forward(g, x, state_in=None, want_state=True, want_carry=False)`` ->
+  ``(y, state_out, carry)``, ``gated_scan_backward(g, x, carry, gy, gstate_out=None)`` ->
+  ``(gg, gx, gstate_in)`` and ``gated_scan_step(g, x, state)`` -> ``y``: the gated linear
+  recurrence, its gradients and one token of it (fp32 or bf16).
 """
 from __future__ import annotations
 
@@ -29,6 +33,7 @@ from . import build as _build
 
 __all__ = [
     "WkvError", "Workspace", "wkv_forward", "wkv_decode_step", "wkv_decode_step_fused", "token_shift_mix",
+    "gated_scan_forward", "gated_scan_backward", "gated_scan_step",
     "workspace_size", "forward_status", "auto_path", "lib", "LIB_PATH", "STATUS",
 ]
 
@@ -80,6 +85,11 @@ def lib():
                 L.eagle_decode_step.argtypes = [i64, i64, i64] + [vp] * 7
                 L.wkv_decode_step_fused.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
                 L.token_shift_mix.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp]
+                L.gated_scan_forward.argtypes = [i64, i64, i64, i32] + [vp] * 7
+                L.gated_scan_backward.argtypes = [i64, i64, i64, i32] + [vp] * 9
+                L.gated_scan_step.argtypes = [i64, i64, i64, i32] + [vp] * 5
+                L.gated_scan_carry_size.argtypes = [i64, i64, i64]
+                L.gated_scan_carry_size.restype = sz
                 L.wkv_status_string.argtypes = [i32]
                 L.wkv_status_string.restype = ctypes.c_char_p
                 L.wkv_forward_auto_path.argtypes = [i64, i64, i64, i32]
@@ -87,7 +97,8 @@ def lib():
                 for f in (L.wkv_forward, L.wkv_forward_ex, L.wkv_workspace_init, L.wkv_forward_status,
                           L.wkv_get_device_status, L.wkv_forward_gated, L.token_shift_mix3, L.wkv_backward,
                           L.wkv_decode_step, L.wkv_decode_step_fused, L.token_shift_mix,
-                          L.wkv_forward_auto_path, L.wkv_testhook_forward_drop):
+                          L.wkv_forward_auto_path, L.wkv_testhook_forward_drop, L.gated_scan_forward,
+                          L.gated_scan_backward, L.gated_scan_step):
                     f.restype = i32
                 _lib = L
     return _lib
@@ -344,3 +355,102 @@ def token_shift_mix(mu, x, x_last=None, xbar=None):
     _check(lib().token_shift_mix(B, T, C, mu.data_ptr(), x.data_ptr(), _ptr(x_last), xbar.data_ptr(),
                                  _stream(x.device)), "token_shift_mix")
     return xbar
+
+
+def _io(t, name, like=None):
+    """Checks an fp32 or bf16 tensor; with `like`, one of its type, shape and device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if like is None:
+        if t.dtype not in _DTYPE:
+            raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    elif t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    elif t.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _launch(fn, tensors, *args):
+    """Calls the library on the tensors' device and its current stream."""
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on one device, got {dev} and {t.device}")
+    if dev.index == torch.cuda.current_device():
+        return _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), fn.__name__)
+    with torch.cuda.device(dev):
+        return _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), fn.__name__)
+
+
+def _btc(g, x):
+    _io(g, "g")
+    if g.dim() != 3:
+        raise ValueError("g must be [B, T, C]")
+    _io(x, "x", like=g)
+    return g.shape
+
+
+def _carry_shape(B, T, C):
+    return (B, (T + 127) // 128, C)
+
+
+def gated_scan_forward(g, x, state_in=None, want_state=True, want_carry=False, y=None, state_out=None, carry=None):
+    """The gated linear recurrence h_t = f_t h_{t-1} + (1 - f_t) x_t, f = sigma(g), over [B, T, C]
+    from state_in [B, C] (None: zeros): returns (y, state_out, carry).  y has g's dtype; state_out
+    is [B, C] fp32 (None unless want_state or given); carry is what gated_scan_backward reads,
+    [B, ceil(T / 128), C] fp32 (None unless want_carry or given)."""
+    B, T, C = _btc(g, x)
+    dev = g.device
+    if state_in is not None:
+        _cuda_f32(state_in, "state_in", (B, C))
+    y = torch.empty_like(g) if y is None else _io(y, "y", like=g)
+    if state_out is not None:
+        _cuda_f32(state_out, "state_out", (B, C))
+    elif want_state:
+        state_out = torch.empty((B, C), dtype=torch.float32, device=dev)
+    if carry is not None:
+        _cuda_f32(carry, "carry", _carry_shape(B, T, C))
+    elif want_carry:
+        carry = torch.empty(_carry_shape(B, T, C), dtype=torch.float32, device=dev)
+    _launch(lib().gated_scan_forward, (g, x, state_in, y, state_out, carry), B, T, C, _DTYPE[g.dtype], g.data_ptr(),
+            x.data_ptr(), _ptr(state_in), y.data_ptr(), _ptr(state_out), _ptr(carry))
+    return y, state_out, carry
+
+
+def gated_scan_backward(g, x, carry, gy, gstate_out=None, want_gstate=True, gg=None, gx=None, gstate_in=None):
+    """Gradients of a loss of gated_scan_forward's y and state_out, given gy [B, T, C] (g's dtype)
+    and gstate_out [B, C] fp32 (None: zeros), with the carry that forward wrote: returns
+    (gg, gx, gstate_in); gstate_in is [B, C] fp32 (None unless want_gstate or given)."""
+    B, T, C = _btc(g, x)
+    _cuda_f32(carry, "carry", _carry_shape(B, T, C))
+    _io(gy, "gy", like=g)
+    if gstate_out is not None:
+        _cuda_f32(gstate_out, "gstate_out", (B, C))
+    gg = torch.empty_like(g) if gg is None else _io(gg, "gg", like=g)
+    gx = torch.empty_like(g) if gx is None else _io(gx, "gx", like=g)
+    if gstate_in is not None:
+        _cuda_f32(gstate_in, "gstate_in", (B, C))
+    elif want_gstate:
+        gstate_in = torch.empty((B, C), dtype=torch.float32, device=g.device)
+    _launch(lib().gated_scan_backward, (g, x, carry, gy, gstate_out, gg, gx, gstate_in), B, T, C, _DTYPE[g.dtype],
+            g.data_ptr(), x.data_ptr(), carry.data_ptr(), gy.data_ptr(), _ptr(gstate_out), gg.data_ptr(),
+            gx.data_ptr(), _ptr(gstate_in))
+    return gg, gx, gstate_in
+
+
+def gated_scan_step(g, x, state, y=None):
+    """One token of the gated linear recurrence for [N, L, C] rows; state [N, L, C] fp32 is updated
+    in place.  Returns y (g's dtype)."""
+    _io(g, "g")
+    if g.dim() != 3:
+        raise ValueError("g must be [N, L, C]")
+    _io(x, "x", like=g)
+    N, L, C = g.shape
+    _cuda_f32(state, "state", (N, L, C))
+    y = torch.empty_like(g) if y is None else _io(y, "y", like=g)
+    _launch(lib().gated_scan_step, (g, x, state, y), N, L, C, _DTYPE[g.dtype], g.data_ptr(), x.data_ptr(),
+            state.data_ptr(), y.data_ptr())
+    return y

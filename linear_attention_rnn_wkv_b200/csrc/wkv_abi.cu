@@ -7,6 +7,7 @@
 #include "wkv.h"
 #include "wkv_device.cuh"
 #include "wkv_eagle_internal.h"
+#include "wkv_gated_internal.h"
 #include "wkv_internal.h"
 #include "wkv_path_table.h"
 
@@ -295,6 +296,53 @@ wkv_status eagle_decode_step(int64_t N, int64_t L, int64_t C, const float* w, co
     if (!f32_args_ok({w, r, k, v, state_inout, y})) return WKV_ERR_MISALIGNED;
     if (n / 64 > INT32_MAX) return WKV_ERR_UNSUPPORTED;  // one block per (row, head)
     cudaError_t e = launch_eagle_decode(N, L, C, w, r, k, v, state_inout, y, stream);
+    return e == cudaSuccess ? WKV_OK : cuda_fail(e);
+}
+
+size_t gated_scan_carry_size(int64_t B, int64_t T, int64_t C) {
+    int64_t n = 0;
+    if (!sizes_ok(B, T, C, &n) || n > INT64_MAX / 64) return 0;
+    return (size_t)(B * ((T + kGatedCarrySteps - 1) / kGatedCarrySteps) * C) * sizeof(float);
+}
+
+wkv_status gated_scan_forward(int64_t B, int64_t T, int64_t C, wkv_dtype io, const void* g, const void* x,
+                              const float* state_in, void* y, float* state_out, float* carry, cudaStream_t stream) {
+    int64_t n = 0;
+    if (!sizes_ok(B, T, C, &n) || n > INT64_MAX / 64) return WKV_ERR_INVALID_ARG;
+    if (io != WKV_F32 && io != WKV_BF16) return WKV_ERR_UNSUPPORTED;
+    if (B == 0 || C == 0) return WKV_OK;
+    if (n > 0 && (!g || !x || !y)) return WKV_ERR_INVALID_ARG;
+    if (!f32_args_ok({g, x, state_in, y, state_out, carry})) return WKV_ERR_MISALIGNED;
+    const GatedScanShape shape{B, T, C, (int)io};
+    if (!gated_scan_fits(shape)) return WKV_ERR_UNSUPPORTED;
+    cudaError_t e = launch_gated_scan_forward(shape, g, x, state_in, y, state_out, carry, stream);
+    return e == cudaSuccess ? WKV_OK : cuda_fail(e);
+}
+
+wkv_status gated_scan_backward(int64_t B, int64_t T, int64_t C, wkv_dtype io, const void* g, const void* x,
+                               const float* carry, const void* gy, const float* gstate_out, void* gg, void* gx,
+                               float* gstate_in, cudaStream_t stream) {
+    int64_t n = 0;
+    if (!sizes_ok(B, T, C, &n) || n > INT64_MAX / 64) return WKV_ERR_INVALID_ARG;
+    if (io != WKV_F32 && io != WKV_BF16) return WKV_ERR_UNSUPPORTED;
+    if (B == 0 || C == 0) return WKV_OK;
+    if (n > 0 && (!g || !x || !carry || !gy || !gg || !gx)) return WKV_ERR_INVALID_ARG;
+    if (!f32_args_ok({g, x, carry, gy, gstate_out, gg, gx, gstate_in})) return WKV_ERR_MISALIGNED;
+    const GatedScanShape shape{B, T, C, (int)io};
+    if (!gated_scan_fits(shape)) return WKV_ERR_UNSUPPORTED;
+    cudaError_t e = launch_gated_scan_backward(shape, g, x, carry, gy, gstate_out, gg, gx, gstate_in, stream);
+    return e == cudaSuccess ? WKV_OK : cuda_fail(e);
+}
+
+wkv_status gated_scan_step(int64_t N, int64_t L, int64_t C, wkv_dtype io, const void* g, const void* x,
+                           float* state_inout, void* y, cudaStream_t stream) {
+    int64_t n = 0;
+    if (!sizes_ok(N, L, C, &n) || n > INT64_MAX / 64) return WKV_ERR_INVALID_ARG;
+    if (io != WKV_F32 && io != WKV_BF16) return WKV_ERR_UNSUPPORTED;
+    if (n == 0) return WKV_OK;
+    if (!g || !x || !state_inout || !y) return WKV_ERR_INVALID_ARG;
+    if (!f32_args_ok({g, x, state_inout, y})) return WKV_ERR_MISALIGNED;
+    cudaError_t e = launch_gated_scan_step(n, (int)io, g, x, state_inout, y, stream);
     return e == cudaSuccess ? WKV_OK : cuda_fail(e);
 }
 

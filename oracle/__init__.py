@@ -31,6 +31,10 @@ Functions (all inputs are converted to contiguous float64):
   per head of N channels.  Returns ``(y, s, state_out)`` (state ``[B, H, N, N]``).
 * ``eagle_direct(w, r, k, v, N=64, state_in=None)`` -- the same outputs summed
   directly over the past (O(T^2 N^2) per head).
+* ``gated_scan(g, x, state_in=None)`` -- the gated linear recurrence
+  ``h_t = sigma(g_t) h_{t-1} + sigma(-g_t) x_t``.  Returns ``(y, s, state_out, s_out)``.
+* ``gated_scan_backward(g, x, gy, state_in=None, gstate_out=None)`` -- its gradients.
+  Returns ``(gg, gx, gstate_in, (sg, sx, ss))``.
 
 ``s`` is the same weighted average with ``|v|`` in place of ``v`` (the error
 scale the parity tests divide by); ``sacc`` is its accumulator in the state.
@@ -76,7 +80,9 @@ def load(path: str):
     L.oracle_wkv_backward_direct.argtypes = [i64, i64, i64] + [vp] * 13
     L.oracle_eagle_recurrent.argtypes = [i64, i64, i64, i64] + [vp] * 8
     L.oracle_eagle_direct.argtypes = [i64, i64, i64, i64] + [vp] * 6
-    for f in (L.oracle_wkv_direct, L.oracle_wkv_recurrent, L.oracle_wkv_naive, L.oracle_token_shift, L.oracle_gate,
+    L.oracle_gated_scan.argtypes = [i64, i64, i64] + [vp] * 7
+    L.oracle_gated_scan_backward.argtypes = [i64, i64, i64] + [vp] * 13
+    for f in (L.oracle_gated_scan, L.oracle_gated_scan_backward, L.oracle_wkv_direct, L.oracle_wkv_recurrent, L.oracle_wkv_naive, L.oracle_token_shift, L.oracle_gate,
               L.oracle_wkv_backward_direct, L.oracle_eagle_recurrent, L.oracle_eagle_direct):
         f.restype = None
     L.oracle_num_threads.restype = ctypes.c_int
@@ -235,3 +241,25 @@ def eagle_direct(w, r, k, v, N=64, state_in=None, L=None):
     y = np.empty(k.shape, np.float64)
     (L or lib()).oracle_eagle_direct(B, T, H, N, _p(w), _p(r), _p(k), _p(v), _p(state_in), _p(y))
     return y
+
+
+def gated_scan(g, x, state_in=None, L=None):
+    g, x = _f64(g), _f64(x)
+    B, T, C = g.shape
+    state_in = None if state_in is None else _f64(state_in)
+    y, s = np.empty(g.shape), np.empty(g.shape)
+    st, ss = np.empty((B, C)), np.empty((B, C))
+    (L or lib()).oracle_gated_scan(B, T, C, _p(g), _p(x), _p(state_in), _p(y), _p(s), _p(st), _p(ss))
+    return y, s, st, ss
+
+
+def gated_scan_backward(g, x, gy, state_in=None, gstate_out=None, L=None):
+    g, x, gy = _f64(g), _f64(x), _f64(gy)
+    B, T, C = g.shape
+    state_in, gstate_out = (None if a is None else _f64(a) for a in (state_in, gstate_out))
+    y, s, _, _ = gated_scan(g, x, state_in, L=L)
+    gg, gx, sg, sx = (np.empty(g.shape) for _ in range(4))
+    gs, ss = np.empty((B, C)), np.empty((B, C))
+    (L or lib()).oracle_gated_scan_backward(B, T, C, _p(g), _p(x), _p(state_in), _p(y), _p(s), _p(gy),
+                                            _p(gstate_out), _p(gg), _p(gx), _p(gs), _p(sg), _p(sx), _p(ss))
+    return gg, gx, gs, (sg, sx, ss)

@@ -405,3 +405,64 @@ void oracle_eagle_direct(int64_t B, int64_t T, int64_t H, int64_t N, const doubl
                 }
         }
 }
+
+/*
+ * Gated linear recurrence, token after token: f = 1 / (1 + e^{-g}), i = 1 / (1 + e^g) = 1 - f,
+ *   h_t = f_t h_{t-1} + i_t x_t,  y_t = h_t,  h_{-1} = state_in ([B][C], NULL: zeros).
+ * s, s_out: the same recurrence on |x| and |state_in| (every value's magnitude scale).
+ */
+void oracle_gated_scan(int64_t B, int64_t T, int64_t C, const double* g, const double* x,
+                       const double* state_in, double* y, double* s, double* state_out, double* s_out)
+{
+#pragma omp parallel for collapse(2) schedule(static)
+    for (int64_t b = 0; b < B; ++b)
+        for (int64_t c = 0; c < C; ++c) {
+            double h = state_in ? state_in[b * C + c] : 0.0, m = fabs(h);
+            for (int64_t t = 0; t < T; ++t) {
+                const size_t e = at3(b, t, c, T, C);
+                const double f = 1.0 / (1.0 + exp(-g[e])), i = 1.0 / (1.0 + exp(g[e]));
+                h = f * h + i * x[e];
+                m = f * m + i * fabs(x[e]);
+                y[e] = h;
+                s[e] = m;
+            }
+            state_out[b * C + c] = h;
+            s_out[b * C + c] = m;
+        }
+}
+
+/*
+ * Its gradients for a loss with dL/dy = gy and dL/dstate_out = gs ([B][C], NULL: zeros): lam_t
+ * the gradient of h_t over all later tokens,
+ *   lam_t = gy_t + f_{t+1} lam_{t+1} (gs after the last),  gx_t = i_t lam_t,
+ *   gg_t = f_t i_t (h_{t-1} - x_t) lam_t,  gstate_in = f_0 lam_0.
+ * sg, sx, ss: the same with |gy|, |gs|, and the magnitude scale of h plus |x| for h - x.
+ * y, s: what oracle_gated_scan gives for these inputs.
+ */
+void oracle_gated_scan_backward(int64_t B, int64_t T, int64_t C, const double* g, const double* x,
+                                const double* state_in, const double* y, const double* s, const double* gy,
+                                const double* gs, double* gg, double* gx, double* gstate_in, double* sg,
+                                double* sx, double* ss)
+{
+#pragma omp parallel for collapse(2) schedule(static)
+    for (int64_t b = 0; b < B; ++b)
+        for (int64_t c = 0; c < C; ++c) {
+            double m = gs ? gs[b * C + c] : 0.0, ms = fabs(m);
+            for (int64_t t = T - 1; t >= 0; --t) {
+                const size_t e = at3(b, t, c, T, C);
+                const double f = 1.0 / (1.0 + exp(-g[e])), i = 1.0 / (1.0 + exp(g[e]));
+                const double h0 = state_in ? state_in[b * C + c] : 0.0;
+                const double before = t > 0 ? y[at3(b, t - 1, c, T, C)] : h0;
+                const double mag = t > 0 ? s[at3(b, t - 1, c, T, C)] : fabs(h0);
+                const double lam = gy[e] + m, lams = fabs(gy[e]) + ms;
+                gx[e] = i * lam;
+                sx[e] = i * lams;
+                gg[e] = f * i * (before - x[e]) * lam;
+                sg[e] = f * i * (mag + fabs(x[e])) * lams;
+                m = f * lam;
+                ms = f * lams;
+            }
+            gstate_in[b * C + c] = m;
+            ss[b * C + c] = ms;
+        }
+}
