@@ -4,7 +4,7 @@
 // A span of steps maps the state entering it to the state leaving it by
 //   h_out = A h_in + H,   A = prod f_t,   H = the span's state from zero,
 // and two adjacent spans compose as (A1 A2, A2 H1 + H2), so the long axis is split: a warp
-// takes kLC consecutive steps of 32 V adjacent channels into registers, sums them up as (A, H),
+// takes LC consecutive steps of 32 V adjacent channels into registers, sums them up as (A, H),
 // and once it knows the state entering its steps runs them again from the registers.  The
 // warps of a block cover a tile of kTile steps, the blocks of a cluster adjacent tiles; a
 // cluster walks its channels' sequence in strides of S tiles and carries the state from stride
@@ -20,25 +20,25 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "wkv_device.cuh"
 #include "wkv_gated_internal.h"
 #include "wkv_internal.h"
+#include "wkv_pipe_common.cuh"
 #include "wkv_vec.cuh"
 
 namespace wkvb {
 namespace {
 
-constexpr int kLC = 8;                    // steps per warp
-constexpr int kNW = 16;                   // warps per block
-constexpr int kThreads = 32 * kNW;
-constexpr int kTile = kLC * kNW;          // steps per tile
+constexpr int kTile = kGatedCarrySteps;   // steps per tile: one saved state each
 constexpr int kMaxCluster = 8;            // portable cluster size
-static_assert(kTile == kGatedCarrySteps, "one saved state per tile");
+constexpr int kRowBytes = 128;            // one row of a staged tile
 
 struct ScanArgs {
     int64_t B, T, C;
     int64_t groups;  // channel groups per sequence
-    int wt_log;      // log2 of the warps of a block along time (kNW unless a shorter tile holds T)
+    int wt_log;      // log2 of the warps of a block along time (NW unless a shorter tile holds T)
     const void *g, *x, *gy;
     const float* state_in;   // forward: [B][C] or null
     void* y;                 // forward: y; backward: gx
@@ -46,6 +46,7 @@ struct ScanArgs {
     float* state_out;        // forward: state_out; backward: gstate_in; [B][C] or null
     float* carry;            // [B][tiles][C]: forward writes (or null), backward reads
     const float* gstate;     // backward: gradient of state_out, [B][C] or null
+    uint32_t* dev_err;       // the library's device-wide error word
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -59,139 +60,339 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return r;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// this block's shared address as the same place in block `rank` of the cluster
-__device__ __forceinline__ void st_cluster_f2(uint32_t saddr, uint32_t rank, float2 v) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(r), "f"(v.x), "f"(v.y) : "memory");
-}
+// ---- V (1 or 2) adjacent channels per lane: scalars, or pairs on the packed fp32 instructions ----
+template <int V>
+struct Lanes;
+template <>
+struct Lanes<1> {
+    using T = float;
+    static __device__ __forceinline__ T all(float a) { return a; }
+    static __device__ __forceinline__ T make(const float (&a)[1]) { return a[0]; }
+    static __device__ __forceinline__ void split(T a, float (&o)[1]) { o[0] = a; }
+};
+template <>
+struct Lanes<2> {
+    using T = float2;
+    static __device__ __forceinline__ T all(float a) { return make_float2(a, a); }
+    static __device__ __forceinline__ T make(const float (&a)[2]) { return make_float2(a[0], a[1]); }
+    static __device__ __forceinline__ void split(T a, float (&o)[2]) {
+        o[0] = a.x;
+        o[1] = a.y;
+    }
+};
+__device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float vmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float2 vmul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float vadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 vadd(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float vsub(float a, float b) { return a - b; }
+__device__ __forceinline__ float2 vsub(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.f, -1.f), a); }
 
-// The signed gate: +i where i = sigma(-g) <= 1/2, -f where f = sigma(g) < 1/2 (the sign is g's,
-// also on a zero).
-__device__ __forceinline__ float signed_gate(float g) {
+// ---- the gate, as one signed number s per token: -i where i = sigma(-g) <= 1/2 ("holds": the
+// state is kept more than replaced), +f where f = sigma(g) < 1/2; the sign is set on a zero too ----
+__device__ __forceinline__ bool holds(float s) { return __float_as_int(s) < 0; }
+__device__ __forceinline__ float with_sign_of_minus(float small, float g) {
+    return __uint_as_float(__float_as_uint(small) | (~__float_as_uint(g) & 0x80000000u));
+}
+__device__ __forceinline__ float gate(float g) {
     const float e = ex2(-fabsf(g) * kLog2e);
-    return copysignf(e * rcp(1.f + e), g);
+    return with_sign_of_minus(e * rcp(1.f + e), g);
 }
-__device__ __forceinline__ bool holds(float s) { return __float_as_int(s) >= 0; }  // i <= 1/2
+__device__ __forceinline__ float2 gate(float2 g) {
+    const float2 e = make_float2(ex2(-fabsf(g.x) * kLog2e), ex2(-fabsf(g.y) * kLog2e));
+    const float2 d = __fadd2_rn(e, make_float2(1.f, 1.f));
+    const float2 small = __fmul2_rn(e, make_float2(rcp(d.x), rcp(d.y)));
+    return make_float2(with_sign_of_minus(small.x, g.x), with_sign_of_minus(small.y, g.y));
+}
+__device__ __forceinline__ float pick(float s, float if_holds, float if_not) { return holds(s) ? if_holds : if_not; }
+__device__ __forceinline__ float2 pick(float2 s, float2 if_holds, float2 if_not) {
+    return make_float2(pick(s.x, if_holds.x, if_not.x), pick(s.y, if_holds.y, if_not.y));
+}
+__device__ __forceinline__ float neg(float a) { return -a; }
+__device__ __forceinline__ float2 neg(float2 a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ float zero(float) { return 0.f; }
+__device__ __forceinline__ float2 zero(float2) { return make_float2(0.f, 0.f); }
 
-// f h + i x
-__device__ __forceinline__ float gate_step(float s, float h, float x) { return fmaf(s, x - h, holds(s) ? h : x); }
-// f a
-__device__ __forceinline__ float gate_decay(float s, float a) { return fmaf(-s, a, holds(s) ? a : 0.f); }
-// i a
-__device__ __forceinline__ float gate_input(float s, float a) { return fmaf(s, a, holds(s) ? 0.f : a); }
+// f h + i x: h - i (h - x), or x + f (h - x)
+template <typename T>
+__device__ __forceinline__ T gate_step(T s, T h, T x) { return vfma(s, vsub(h, x), pick(s, h, x)); }
+// f a: a - i a, or f a
+template <typename T>
+__device__ __forceinline__ T gate_decay(T s, T a) { return vfma(s, a, pick(s, a, zero(a))); }
+// -i a: -i a, or f a - a
+template <typename T>
+__device__ __forceinline__ T gate_input_neg(T s, T a) { return vfma(s, a, pick(s, zero(a), neg(a))); }
+// -f i = s^2 - |s|
+__device__ __forceinline__ float gate_slope_neg(float s) { return fmaf(fabsf(s), fabsf(s), -fabsf(s)); }
+__device__ __forceinline__ float2 gate_slope_neg(float2 s) { return make_float2(gate_slope_neg(s.x), gate_slope_neg(s.y)); }
 
-// V adjacent channels of kLC rows (row stride C elements) as fp32; rows from n on are not read and
-// come back as `fill`
-template <typename TIO, int V>
-__device__ __forceinline__ void load_rows(const TIO* p, int64_t C, int n, float fill, float (&o)[kLC][V]) {
+// V adjacent channels of LC rows (`stride` elements apart) as fp32; rows from n on are not read
+// and come back as `fill`
+template <typename TIO, int V, int LC, bool ALL>
+__device__ __forceinline__ void load_rows(const TIO* p, int64_t stride, int n, float fill, typename Lanes<V>::T (&o)[LC]) {
 #pragma unroll
-    for (int s = 0; s < kLC; ++s) {
+    for (int s = 0; s < LC; ++s) {
+        float t[V];
+        if (ALL || s < n) {
+            Vec<TIO, V>::load(p + s * stride, t);
+        } else {
 #pragma unroll
-        for (int q = 0; q < V; ++q) o[s][q] = fill;
-        if (s < n) Vec<TIO, V>::load(p + s * C, o[s]);
+            for (int q = 0; q < V; ++q) t[q] = fill;
+        }
+        o[s] = Lanes<V>::make(t);
     }
 }
 
-template <typename TIO, int V>
-__global__ void __launch_bounds__(kThreads) scan_fwd(ScanArgs a) {
-    __shared__ float2 wsum[2][kNW * 32 * V];           // the warps' (A, H), [time warp][channel]
-    __shared__ float2 csum[2][kMaxCluster][32 * V];    // the cluster's blocks' (A, H)
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int WT = 1 << a.wt_log, wt = warp & (WT - 1), wc = warp >> a.wt_log;
-    const int W = (kNW >> a.wt_log) * 32 * V;          // channels of this block
-    const int cl = (wc * 32 + lane) * V;               // this lane's first, within the block
-    const uint32_t S = cluster_size(), rank = cluster_rank();
-    const int64_t unit = blockIdx.x / S, b = unit / a.groups;
-    const int64_t c = (unit % a.groups) * W + cl;
-    const bool live = c < a.C;
-    const int64_t tile = (int64_t)WT * kLC, tiles = (a.T + tile - 1) / tile;
+// A ring of ST staged tiles (ST = 0: none, the lanes read global memory): one TMA box of ROWS
+// rows of 32 V channels per array, completion on the slot's barrier.  Thread 0 refills a slot
+// right after the block's barrier behind which every lane has its values in registers.
+template <int ARRAYS, int ST, int BOX>
+struct Ring {
+    unsigned char* slots;
+    uint64_t* full;
+    int c0, b;
+
+    __device__ __forceinline__ void init() {
+        for (int i = 0; i < ST; ++i) mbar_init(&full[i], 1);
+    }
+    // the tile at step t0 into slot it % ST
+    __device__ __forceinline__ void fetch(int it, int64_t t0, const CUtensorMap* const (&maps)[ARRAYS]) {
+        const int slot = it % ST;
+        mbar_arrive_expect_tx(&full[slot], ARRAYS * BOX);
+#pragma unroll
+        for (int k = 0; k < ARRAYS; ++k)
+            tma_load_3d(slots + (size_t)(slot * ARRAYS + k) * BOX, maps[k], c0, (int)t0, b, &full[slot]);
+    }
+    __device__ __forceinline__ bool wait(int it) { return mbar_wait(&full[it % ST], (it / ST) & 1, kSpinLimitDefault); }
+    template <typename TIO>
+    __device__ __forceinline__ const TIO* array(int it, int k) const {
+        return reinterpret_cast<const TIO*>(slots + (size_t)(it % ST * ARRAYS + k) * BOX);
+    }
+};
+
+// The blocks' summaries of one stride, in every block of the cluster: each block sends its own
+// to all (st.async: the data and its arrival on the receiver's barrier travel together, so no
+// fence has to wait for the outputs still being written).  Two buffers: a block sends stride
+// it + 2 only after it has everyone's stride it + 1, and those were sent after their senders
+// had read stride it.
+template <typename P>
+struct Exchange {
+    P (*sum)[kMaxCluster][32];
+    uint64_t* bar;
+
+    __device__ __forceinline__ void init() {
+        mbar_init(&bar[0], 1);
+        mbar_init(&bar[1], 1);
+    }
+    __device__ __forceinline__ void expect(int it, uint32_t S) {
+        mbar_arrive_expect_tx(&bar[it & 1], S * 32 * (uint32_t)sizeof(P));
+    }
+    __device__ __forceinline__ void send(int it, uint32_t S, uint32_t rank, int lane, const P& p) {
+        const uint32_t at = smem_u32(&sum[it & 1][rank][lane]), on = smem_u32(&bar[it & 1]);
+        for (uint32_t k = 0; k < S; ++k) {
+            uint32_t rat, ron;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rat) : "r"(at), "r"(k));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ron) : "r"(on), "r"(k));
+            send_to(rat, ron, p);
+        }
+    }
+    static __device__ __forceinline__ void send_to(uint32_t at, uint32_t on, const float2& p) {
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at),
+                     "f"(p.x), "f"(p.y), "r"(on)
+                     : "memory");
+    }
+    static __device__ __forceinline__ void send_to(uint32_t at, uint32_t on, const float4& p) {
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+                     "f"(p.x), "f"(p.y), "f"(p.z), "f"(p.w), "r"(on)
+                     : "memory");
+    }
+    __device__ __forceinline__ bool wait(int it) { return mbar_wait(&bar[it & 1], (it >> 1) & 1, kSpinLimitDefault); }
+};
+
+// (A, H) of a span, V channels, as one vector
+template <int V>
+struct Span;
+template <>
+struct Span<1> {
+    using P = float2;
+    static __device__ __forceinline__ P pack(float A, float H) { return make_float2(A, H); }
+    static __device__ __forceinline__ float A(const P& p) { return p.x; }
+    static __device__ __forceinline__ float H(const P& p) { return p.y; }
+};
+template <>
+struct Span<2> {
+    using P = float4;
+    static __device__ __forceinline__ P pack(float2 A, float2 H) { return make_float4(A.x, A.y, H.x, H.y); }
+    static __device__ __forceinline__ float2 A(const P& p) { return make_float2(p.x, p.y); }
+    static __device__ __forceinline__ float2 H(const P& p) { return make_float2(p.z, p.w); }
+};
+
+// What both directions share: where a lane's channels and steps lie, the hand-over of the state.
+template <typename TIO, int V, int LC, int NW, int ST, int ARRAYS>
+struct Block {
+    using T = typename Lanes<V>::T;
+    using P = typename Span<V>::P;
+    static constexpr int kBox = LC * NW * 32 * V * (int)sizeof(TIO);
+    const ScanArgs& a;
+    int lane, warp, WT, wt, W, cl;
+    uint32_t S, rank;
+    int64_t b, c, tile, tiles;
+    bool live, whole;  // this lane's channels exist; so do all of its warp's
+
+    __device__ __forceinline__ Block(const ScanArgs& args) : a(args) {
+        lane = threadIdx.x & 31;
+        warp = threadIdx.x >> 5;
+        WT = ST ? NW : 1 << a.wt_log;
+        wt = ST ? warp : warp & (WT - 1);
+        const int wc = ST ? 0 : warp >> a.wt_log;
+        W = ST ? 32 * V : (NW >> a.wt_log) * 32 * V;
+        cl = (wc * 32 + lane) * V;
+        S = cluster_size();
+        rank = cluster_rank();
+        const int64_t unit = blockIdx.x / S;
+        b = unit / a.groups;
+        c = (unit % a.groups) * W + cl;
+        live = c < a.C;
+        whole = c - lane * V + 32 * V <= a.C;
+        tile = (int64_t)WT * LC;
+        tiles = (a.T + tile - 1) / tile;
+    }
+    __device__ __forceinline__ T load_state(const float* p, int64_t row) const {
+        float t[V];
+#pragma unroll
+        for (int q = 0; q < V; ++q) t[q] = p && live ? p[row * a.C + c + q] : 0.f;
+        return Lanes<V>::make(t);
+    }
+    __device__ __forceinline__ void store_state(float* p, int64_t row, T v) const {
+        float t[V];
+        Lanes<V>::split(v, t);
+        if (p && live)
+#pragma unroll
+            for (int q = 0; q < V; ++q) p[row * a.C + c + q] = t[q];
+    }
+    __device__ __forceinline__ void gave_up() const {
+        atomicCAS(a.dev_err, kDevOk, (uint32_t)kDevTimeoutCopy);
+    }
+};
+
+template <typename TIO, int V, int LC, int NW, int ST>
+__global__ void __launch_bounds__(32 * NW) scan_fwd(ScanArgs a, const __grid_constant__ CUtensorMap mg,
+                                                    const __grid_constant__ CUtensorMap mx) {
+    using B = Block<TIO, V, LC, NW, ST, 2>;
+    using T = typename B::T;
+    using P = typename B::P;
+    using Sp = Span<V>;
+    extern __shared__ __align__(1024) unsigned char slots[];
+    __shared__ P wsum[2][NW][32];  // the warps' (A, H)
+    __shared__ P csum[2][kMaxCluster][32];
+    __shared__ uint64_t bars[(ST ? ST : 1) + 2];
+    const B k(a);
+    Ring<2, ST ? ST : 1, B::kBox> ring{slots, bars + 2, (int)(k.c - k.cl), (int)k.b};
+    Exchange<P> ex{csum, bars};
+    const CUtensorMap* const maps[2] = {&mg, &mx};
+    const int64_t tiles = k.tiles;
+    const uint32_t S = k.S, rank = k.rank;
     grid_dep_launch_dependents();
+    if (threadIdx.x == 0) {
+        ex.init();
+        if (ST) ring.init();
+        fence_mbar_init();
+    }
+    __syncwarp();
     if (S > 1) cluster_arrive();
     grid_dep_wait();  // before any global memory access
-    float carry[V];
-#pragma unroll
-    for (int q = 0; q < V; ++q) carry[q] = live && a.state_in ? a.state_in[b * a.C + c + q] : 0.f;
-    if (S > 1) cluster_wait();  // every block of the cluster runs: its shared memory may be written
-
-    int buf = 0;
-    for (int64_t j0 = 0; j0 < tiles; j0 += S, buf ^= 1) {
-        const int64_t j = j0 + rank, t0 = j * tile + wt * kLC;
-        const int n = live && t0 < a.T ? (int)min64(kLC, a.T - t0) : 0;
-        const int64_t at = (b * a.T + t0) * a.C + c;
-        float sg[kLC][V], x[kLC][V];
-        load_rows<TIO, V>(static_cast<const TIO*>(a.g) + at, a.C, n, INFINITY, sg);  // i = 0: the state stays
-        load_rows<TIO, V>(static_cast<const TIO*>(a.x) + at, a.C, n, 0.f, x);
-        float A[V], H[V];
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-            A[q] = 1.f;
-            H[q] = 0.f;
-        }
-#pragma unroll
-        for (int s = 0; s < kLC; ++s)
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                sg[s][q] = signed_gate(sg[s][q]);
-                A[q] = gate_decay(sg[s][q], A[q]);
-                H[q] = gate_step(sg[s][q], H[q], x[s][q]);
-            }
-#pragma unroll
-        for (int q = 0; q < V; ++q) wsum[buf][wt * W + cl + q] = make_float2(A[q], H[q]);
+    if (ST && threadIdx.x == 0)
+        for (int it = 0; it < ST && (int64_t)it * S + rank < tiles; ++it) ring.fetch(it, (it * (int64_t)S + rank) * k.tile, maps);
+    T carry = k.load_state(a.state_in, k.b);
+    if (S > 1)
+        cluster_wait();  // every block of the cluster runs and its barriers are ready
+    else
         __syncthreads();
+
+    int it = 0;
+    auto stride = [&](auto all, int64_t j, int64_t t0, int n) {
+        constexpr bool ALL = decltype(all)::value;
+        const int64_t at = (k.b * a.T + t0) * a.C + k.c;
+        T sg[LC], x[LC];
+        if (ST) {  // rows past T and channels past C came as zeros
+            load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 0) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, sg);
+            load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 1) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, x);
+        } else {
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.g) + at, a.C, n, 0.f, sg);
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.x) + at, a.C, n, 0.f, x);
+        }
+        T A = Lanes<V>::all(1.f), H = Lanes<V>::all(0.f);
+#pragma unroll
+        for (int s = 0; s < LC; ++s) {
+            sg[s] = gate(sg[s]);
+            if (!ALL && s >= n) {  // no such token: the state stays
+                sg[s] = Lanes<V>::all(-0.f);
+                x[s] = Lanes<V>::all(0.f);
+            }
+            A = gate_decay(sg[s], A);
+            H = gate_step(sg[s], H, x[s]);
+        }
+        P(*ws)[32] = wsum[it & 1];
+        ws[k.warp][k.lane] = Sp::pack(A, H);
+        if (S > 1 && threadIdx.x == 0) ex.expect(it, S);
+        __syncthreads();
+        if (ST && threadIdx.x == 0 && j + (int64_t)ST * S < tiles) ring.fetch(it + ST, (j + (int64_t)ST * S) * k.tile, maps);
+        const int w0 = k.warp - k.wt;  // this warp's channels: warps w0 .. w0 + WT - 1 in time order
+        T h = carry;
         if (S > 1) {
-            if (wt == 0) {  // the block's (A, H), to every block of the cluster
-#pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    float2 tot = make_float2(1.f, 0.f);
-                    for (int k = 0; k < WT; ++k) {
-                        const float2 r = wsum[buf][k * W + cl + q];
-                        tot = make_float2(tot.x * r.x, fmaf(r.x, tot.y, r.y));
-                    }
-                    const uint32_t at_s = smem_u32(&csum[buf][rank][cl + q]);
-                    for (uint32_t k = 0; k < S; ++k) st_cluster_f2(at_s, k, tot);
+            if (k.wt == 0) {
+                T tA = Sp::A(ws[w0][k.lane]), tH = Sp::H(ws[w0][k.lane]);
+                for (int w = 1; w < k.WT; ++w) {
+                    const P p = ws[w0 + w][k.lane];
+                    tA = vmul(tA, Sp::A(p));
+                    tH = vfma(Sp::A(p), tH, Sp::H(p));
                 }
+                ex.send(it, S, rank, k.lane, Sp::pack(tA, tH));
             }
-            cluster_arrive();
-            cluster_wait();
-        }
-        float h[V];
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-            h[q] = carry[q];
-            if (S > 1) {
-                for (uint32_t k = 0; k < S; ++k) {
-                    const float2 r = csum[buf][k][cl + q];
-                    carry[q] = fmaf(r.x, carry[q], r.y);
-                    if (k + 1 == rank) h[q] = carry[q];
-                }
-                for (int k = 0; k < wt; ++k) {
-                    const float2 r = wsum[buf][k * W + cl + q];
-                    h[q] = fmaf(r.x, h[q], r.y);
-                }
-            } else {
-                for (int k = 0; k < WT; ++k) {
-                    const float2 r = wsum[buf][k * W + cl + q];
-                    carry[q] = fmaf(r.x, carry[q], r.y);
-                    if (k + 1 == wt) h[q] = carry[q];
-                }
+            if (!ex.wait(it) && k.lane == 0) k.gave_up();
+            for (uint32_t r = 0; r < S; ++r) {
+                if (r == rank) h = carry;
+                const P p = csum[it & 1][r][k.lane];
+                carry = vfma(Sp::A(p), carry, Sp::H(p));
+            }
+            for (int w = 0; w < k.wt; ++w) {
+                const P p = ws[w0 + w][k.lane];
+                h = vfma(Sp::A(p), h, Sp::H(p));
+            }
+        } else {
+            for (int w = 0; w < k.WT; ++w) {
+                if (w == k.wt) h = carry;
+                const P p = ws[w0 + w][k.lane];
+                carry = vfma(Sp::A(p), carry, Sp::H(p));
             }
         }
-        if (a.carry && wt == 0 && live && j < tiles)
-#pragma unroll
-            for (int q = 0; q < V; ++q) a.carry[(b * tiles + j) * a.C + c + q] = h[q];
+        if (a.carry && k.wt == 0 && j < tiles) k.store_state(a.carry, k.b * tiles + j, h);
         TIO* y = static_cast<TIO*>(a.y) + at;
 #pragma unroll
-        for (int s = 0; s < kLC; ++s) {
-#pragma unroll
-            for (int q = 0; q < V; ++q) h[q] = gate_step(sg[s][q], h[q], x[s][q]);
-            if (s < n) Vec<TIO, V>::store(y + s * a.C, h);
+        for (int s = 0; s < LC; ++s) {
+            h = gate_step(sg[s], h, x[s]);
+            float o[V];
+            Lanes<V>::split(h, o);
+            if (ALL || s < n) Vec<TIO, V>::store(y + s * a.C, o);
         }
+    };
+    for (int64_t j0 = 0; j0 < tiles; j0 += S, ++it) {
+        const int64_t j = j0 + rank, t0 = j * k.tile + k.wt * LC;
+        if (ST && j < tiles && !ring.wait(it) && k.lane == 0) k.gave_up();
+        if (k.whole && t0 + LC <= a.T)
+            stride(std::true_type{}, j, t0, LC);
+        else
+            stride(std::false_type{}, j, t0, k.live && t0 < a.T ? (int)min64(LC, a.T - t0) : 0);
     }
-    if (a.state_out && rank == 0 && wt == 0 && live)
-#pragma unroll
-        for (int q = 0; q < V; ++q) a.state_out[b * a.C + c + q] = carry[q];
+    if (rank == 0 && k.wt == 0) k.store_state(a.state_out, k.b, carry);
+    if (S > 1) {  // no block leaves while another may still send to it
+        __syncwarp();
+        cluster_arrive_relaxed();
+        cluster_wait();
+    }
 }
 
 // Gradients, in reverse time.  With m_t the gradient reaching h_t from the later tokens
@@ -200,130 +401,146 @@ __global__ void __launch_bounds__(kThreads) scan_fwd(ScanArgs a) {
 // A span maps m by m_out = A m_in + M with the forward's A, so the split over warps, blocks and
 // strides is the forward's mirrored.  h_{t-1} comes from the tile's saved entering state and the
 // forward recurrence of the tile's own steps (the warps' H, exchanged together with M): g, x and
-// gy are read once and no other per-token value is needed.
-template <typename TIO, int V>
-__global__ void __launch_bounds__(kThreads) scan_bwd(ScanArgs a) {
-    __shared__ float wa[2][kNW * 32 * V], wh[2][kNW * 32 * V], wm[2][kNW * 32 * V];
-    __shared__ float2 csum[2][kMaxCluster][32 * V];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int WT = 1 << a.wt_log, wt = warp & (WT - 1), wc = warp >> a.wt_log;
-    const int W = (kNW >> a.wt_log) * 32 * V;
-    const int cl = (wc * 32 + lane) * V;
-    const uint32_t S = cluster_size(), rank = cluster_rank();
-    const int64_t unit = blockIdx.x / S, b = unit / a.groups;
-    const int64_t c = (unit % a.groups) * W + cl;
-    const bool live = c < a.C;
-    const int64_t tile = (int64_t)WT * kLC, tiles = (a.T + tile - 1) / tile;
+// gy are read once and no other per-token value is needed.  m, lam and M are kept negated: every
+// product then is one of s with no sign change on a packed operand.
+template <typename TIO, int V, int LC, int NW, int ST>
+__global__ void __launch_bounds__(32 * NW) scan_bwd(ScanArgs a, const __grid_constant__ CUtensorMap mg,
+                                                    const __grid_constant__ CUtensorMap mx,
+                                                    const __grid_constant__ CUtensorMap mgy) {
+    using B = Block<TIO, V, LC, NW, ST, 3>;
+    using T = typename B::T;
+    using P = typename B::P;
+    using Sp = Span<V>;
+    extern __shared__ __align__(1024) unsigned char slots[];
+    __shared__ P wsum[2][NW][32];  // the warps' (A, H)
+    __shared__ T wadj[2][NW][32];  // and M
+    __shared__ P csum[2][kMaxCluster][32];
+    __shared__ uint64_t bars[(ST ? ST : 1) + 2];
+    const B k(a);
+    Ring<3, ST ? ST : 1, B::kBox> ring{slots, bars + 2, (int)(k.c - k.cl), (int)k.b};
+    Exchange<P> ex{csum, bars};
+    const CUtensorMap* const maps[3] = {&mg, &mx, &mgy};
+    const int64_t tiles = k.tiles;
+    const uint32_t S = k.S, rank = k.rank;
     grid_dep_launch_dependents();
+    if (threadIdx.x == 0) {
+        ex.init();
+        if (ST) ring.init();
+        fence_mbar_init();
+    }
+    __syncwarp();
     if (S > 1) cluster_arrive();
     grid_dep_wait();  // before any global memory access
-    float carry[V];
-#pragma unroll
-    for (int q = 0; q < V; ++q) carry[q] = live && a.gstate ? a.gstate[b * a.C + c + q] : 0.f;
-    if (S > 1) cluster_wait();
-
-    int buf = 0;
-    for (int64_t j0 = 0; j0 < tiles; j0 += S, buf ^= 1) {
-        const int64_t j = tiles - 1 - j0 - rank;  // < 0: past the sequence's start
-        const int64_t t0 = j * tile + wt * kLC;
-        const int n = live && j >= 0 && t0 < a.T ? (int)min64(kLC, a.T - t0) : 0;
-        const int64_t at = (b * a.T + t0) * a.C + c;
-        float sg[kLC][V], x[kLC][V], gy[kLC][V], h[V];
-        load_rows<TIO, V>(static_cast<const TIO*>(a.g) + at, a.C, n, INFINITY, sg);
-        load_rows<TIO, V>(static_cast<const TIO*>(a.x) + at, a.C, n, 0.f, x);
-        load_rows<TIO, V>(static_cast<const TIO*>(a.gy) + at, a.C, n, 0.f, gy);
-#pragma unroll
-        for (int q = 0; q < V; ++q) h[q] = live && j >= 0 ? a.carry[(b * tiles + j) * a.C + c + q] : 0.f;
-        float A[V], H[V], M[V];
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-            A[q] = 1.f;
-            H[q] = 0.f;
-            M[q] = 0.f;
-        }
-#pragma unroll
-        for (int s = 0; s < kLC; ++s)
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                sg[s][q] = signed_gate(sg[s][q]);
-                A[q] = gate_decay(sg[s][q], A[q]);
-                H[q] = gate_step(sg[s][q], H[q], x[s][q]);
-            }
-#pragma unroll
-        for (int s = kLC - 1; s >= 0; --s)
-#pragma unroll
-            for (int q = 0; q < V; ++q) M[q] = gate_decay(sg[s][q], gy[s][q] + M[q]);
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-            wa[buf][wt * W + cl + q] = A[q];
-            wh[buf][wt * W + cl + q] = H[q];
-            wm[buf][wt * W + cl + q] = M[q];
-        }
+    if (ST && threadIdx.x == 0)
+        for (int it = 0; it < ST; ++it)
+            if (const int64_t j = tiles - 1 - it * (int64_t)S - rank; j >= 0) ring.fetch(it, j * k.tile, maps);
+    T carry = neg(k.load_state(a.gstate, k.b));
+    if (S > 1)
+        cluster_wait();
+    else
         __syncthreads();
+
+    int it = 0;
+    auto stride = [&](auto all, int64_t j, int64_t t0, int n) {
+        constexpr bool ALL = decltype(all)::value;
+        const int64_t at = (k.b * a.T + t0) * a.C + k.c;
+        T sg[LC], x[LC], gy[LC];
+        T h = j >= 0 ? k.load_state(a.carry, k.b * tiles + j) : Lanes<V>::all(0.f);
+        if (ST) {
+            load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 0) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, sg);
+            load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 1) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, x);
+            load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 2) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, gy);
+        } else {
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.g) + at, a.C, n, 0.f, sg);
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.x) + at, a.C, n, 0.f, x);
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.gy) + at, a.C, n, 0.f, gy);
+        }
+        T A = Lanes<V>::all(1.f), H = Lanes<V>::all(0.f), M = Lanes<V>::all(0.f);
+#pragma unroll
+        for (int s = 0; s < LC; ++s) {
+            sg[s] = gate(sg[s]);
+            if (!ALL && s >= n) {
+                sg[s] = Lanes<V>::all(-0.f);
+                x[s] = Lanes<V>::all(0.f);
+                gy[s] = Lanes<V>::all(0.f);
+            }
+            A = gate_decay(sg[s], A);
+            H = gate_step(sg[s], H, x[s]);
+        }
+#pragma unroll
+        for (int s = LC - 1; s >= 0; --s) M = gate_decay(sg[s], vsub(M, gy[s]));
+        P(*ws)[32] = wsum[it & 1];
+        T(*wm)[32] = wadj[it & 1];
+        ws[k.warp][k.lane] = Sp::pack(A, H);
+        wm[k.warp][k.lane] = M;
+        if (S > 1 && threadIdx.x == 0) ex.expect(it, S);
+        __syncthreads();
+        if (ST && threadIdx.x == 0 && j - (int64_t)ST * S >= 0) ring.fetch(it + ST, (j - (int64_t)ST * S) * k.tile, maps);
+        const int w0 = k.warp - k.wt;
+        T m = carry;
         if (S > 1) {
-            if (wt == 0) {
-#pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    float2 tot = make_float2(1.f, 0.f);
-                    for (int k = WT - 1; k >= 0; --k) {
-                        const float ak = wa[buf][k * W + cl + q];
-                        tot = make_float2(tot.x * ak, fmaf(ak, tot.y, wm[buf][k * W + cl + q]));
-                    }
-                    const uint32_t at_s = smem_u32(&csum[buf][rank][cl + q]);
-                    for (uint32_t k = 0; k < S; ++k) st_cluster_f2(at_s, k, tot);
+            if (k.wt == 0) {
+                T tA = Lanes<V>::all(1.f), tM = Lanes<V>::all(0.f);
+                for (int w = k.WT - 1; w >= 0; --w) {
+                    const T wA = Sp::A(ws[w0 + w][k.lane]);
+                    tA = vmul(tA, wA);
+                    tM = vfma(wA, tM, wm[w0 + w][k.lane]);
                 }
+                ex.send(it, S, rank, k.lane, Sp::pack(tA, tM));
             }
-            cluster_arrive();
-            cluster_wait();
-        }
-        float m[V];
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-            for (int k = 0; k < wt; ++k) h[q] = fmaf(wa[buf][k * W + cl + q], h[q], wh[buf][k * W + cl + q]);
-            m[q] = carry[q];
-            if (S > 1) {
-                for (uint32_t k = 0; k < S; ++k) {
-                    const float2 r = csum[buf][k][cl + q];
-                    carry[q] = fmaf(r.x, carry[q], r.y);
-                    if (k + 1 == rank) m[q] = carry[q];
-                }
-                for (int k = WT - 1; k > wt; --k) m[q] = fmaf(wa[buf][k * W + cl + q], m[q], wm[buf][k * W + cl + q]);
-            } else {
-                for (int k = WT - 1; k >= 0; --k) {
-                    carry[q] = fmaf(wa[buf][k * W + cl + q], carry[q], wm[buf][k * W + cl + q]);
-                    if (k - 1 == wt) m[q] = carry[q];
-                }
+            if (!ex.wait(it) && k.lane == 0) k.gave_up();
+            for (uint32_t r = 0; r < S; ++r) {
+                if (r == rank) m = carry;
+                const P p = csum[it & 1][r][k.lane];
+                carry = vfma(Sp::A(p), carry, Sp::H(p));
+            }
+            for (int w = k.WT - 1; w > k.wt; --w) m = vfma(Sp::A(ws[w0 + w][k.lane]), m, wm[w0 + w][k.lane]);
+        } else {
+            for (int w = k.WT - 1; w >= 0; --w) {
+                if (w == k.wt) m = carry;
+                carry = vfma(Sp::A(ws[w0 + w][k.lane]), carry, wm[w0 + w][k.lane]);
             }
         }
+        for (int w = 0; w < k.wt; ++w) {
+            const P p = ws[w0 + w][k.lane];
+            h = vfma(Sp::A(p), h, Sp::H(p));
+        }
 #pragma unroll
-        for (int s = 0; s < kLC; ++s)
-#pragma unroll
-            for (int q = 0; q < V; ++q) {  // x becomes f i (h_{t-1} - x_t); f i = |s| (1 - |s|)
-                const float before = h[q], small = fabsf(sg[s][q]);
-                h[q] = gate_step(sg[s][q], before, x[s][q]);
-                x[s][q] = fmaf(-small, small, small) * (before - x[s][q]);
-            }
+        for (int s = 0; s < LC; ++s) {  // x becomes f i (x_t - h_{t-1})
+            const T d = vsub(h, x[s]);
+            h = vfma(sg[s], d, pick(sg[s], h, x[s]));
+            x[s] = vmul(gate_slope_neg(sg[s]), d);
+        }
         TIO* gx = static_cast<TIO*>(a.y) + at;
         TIO* gg = static_cast<TIO*>(a.gg) + at;
 #pragma unroll
-        for (int s = kLC - 1; s >= 0; --s) {
+        for (int s = LC - 1; s >= 0; --s) {
+            const T lam = vsub(m, gy[s]);  // negated, as m
             float ox[V], og[V];
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float lam = gy[s][q] + m[q];
-                ox[q] = gate_input(sg[s][q], lam);
-                og[q] = x[s][q] * lam;
-                m[q] = gate_decay(sg[s][q], lam);
-            }
-            if (s < n) {
+            Lanes<V>::split(gate_input_neg(sg[s], lam), ox);
+            Lanes<V>::split(vmul(x[s], lam), og);
+            m = gate_decay(sg[s], lam);
+            if (ALL || s < n) {
                 Vec<TIO, V>::store(gx + s * a.C, ox);
                 Vec<TIO, V>::store(gg + s * a.C, og);
             }
         }
+    };
+    for (int64_t j0 = 0; j0 < tiles; j0 += S, ++it) {
+        const int64_t j = tiles - 1 - j0 - rank;  // < 0: past the sequence's start
+        const int64_t t0 = j * k.tile + k.wt * LC;
+        if (ST && j >= 0 && !ring.wait(it) && k.lane == 0) k.gave_up();
+        if (k.whole && j >= 0 && t0 + LC <= a.T)
+            stride(std::true_type{}, j, t0, LC);
+        else
+            stride(std::false_type{}, j, t0, k.live && j >= 0 && t0 < a.T ? (int)min64(LC, a.T - t0) : 0);
     }
-    if (a.state_out && rank == 0 && wt == 0 && live)
-#pragma unroll
-        for (int q = 0; q < V; ++q) a.state_out[b * a.C + c + q] = carry[q];
+    if (rank == 0 && k.wt == 0) k.store_state(a.state_out, k.b, neg(carry));
+    if (S > 1) {
+        __syncwarp();
+        cluster_arrive_relaxed();
+        cluster_wait();
+    }
 }
 
 // One token per row-channel: h <- f h + i x, y = h.  Bound by the bytes of g, x, y and the
@@ -340,7 +557,7 @@ __global__ void __launch_bounds__(256) step_kernel(int64_t n, const TIO* __restr
         Vec<TIO, V>::load(x + k, xv);
         Vec<float, V>::load(state + k, h);
 #pragma unroll
-        for (int q = 0; q < V; ++q) h[q] = gate_step(signed_gate(gv[q]), h[q], xv[q]);
+        for (int q = 0; q < V; ++q) h[q] = gate_step(gate(gv[q]), h[q], xv[q]);
         Vec<float, V>::store(state + k, h);
         Vec<TIO, V>::store(y + k, h);
     }
@@ -364,25 +581,39 @@ int sm_count() {
     return sms;
 }
 
-ScanGeom scan_geometry(const GatedScanShape& s, int V) {
+ScanGeom scan_geometry(const GatedScanShape& s, int V, int LC, int NW, int most_blocks) {
     ScanGeom g;
     g.wt_log = 0;
-    while ((1 << g.wt_log) < kNW && (int64_t)(kLC << g.wt_log) < s.T) ++g.wt_log;
-    const int64_t W = (int64_t)(kNW >> g.wt_log) * 32 * V;
+    while ((1 << g.wt_log) < NW && (int64_t)(LC << g.wt_log) < s.T) ++g.wt_log;
+    const int64_t W = (int64_t)(NW >> g.wt_log) * 32 * V;
     g.groups = (s.C + W - 1) / W;
-    const int64_t units = s.B * g.groups, tiles = (s.T + kTile - 1) / kTile;
+    const int64_t units = s.B * g.groups, tiles = (s.T + LC * NW - 1) / (LC * NW);
     g.S = 1;
-    while (g.S < kMaxCluster && g.S < tiles && units * g.S < 2 * sm_count()) g.S *= 2;
+    while (g.S < kMaxCluster && g.S < tiles && units * g.S * 2 <= most_blocks) g.S *= 2;
     g.blocks = units * g.S;
     return g;
 }
 
-template <typename... KArgs>
-cudaError_t launch_cluster(void (*kern)(KArgs...), const ScanGeom& g, const ScanArgs& a, cudaStream_t s) {
+template <typename TIO, int V, int LC, int NW, int ST>
+cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, bool backward, cudaStream_t stream) {
+    const int arrays = backward ? 3 : 2;
+    const int smem = ST * arrays * LC * NW * 32 * V * (int)sizeof(TIO);
+    ScanGeom g = scan_geometry(s, V, LC, NW, TUNE_BLOCKS);
+    a.groups = g.groups;
+    a.wt_log = g.wt_log;
+    CUtensorMap m[3] = {};
+    if (ST) {
+        const void* from[3] = {a.g, a.x, a.gy};
+        g.wt_log = 0;
+        for (int k = 0; k < arrays; ++k)
+            if (!make_tile_map(&m[k], from[k], s.B, s.T, s.C, s.io, 32 * V, LC * NW))
+                return cudaErrorInvalidValue;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)g.blocks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
+    cfg.blockDim = dim3(32 * NW);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch ? 1 : 0;
@@ -390,23 +621,26 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), const ScanGeom& g, const Scan
     at[1].val.clusterDim = {(unsigned)g.S, 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    if (backward) {
+        auto kern = scan_bwd<TIO, V, LC, NW, ST>;
+        if (smem) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaLaunchKernelEx(&cfg, kern, a, m[0], m[1], m[2]);
+    }
+    auto kern = scan_fwd<TIO, V, LC, NW, ST>;
+    if (smem) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaLaunchKernelEx(&cfg, kern, a, m[0], m[1]);
 }
 
-template <typename TIO, int V>
-cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, bool backward, cudaStream_t stream) {
-    const ScanGeom g = scan_geometry(s, V);
-    a.groups = g.groups;
-    a.wt_log = g.wt_log;
-    return launch_cluster(backward ? scan_bwd<TIO, V> : scan_fwd<TIO, V>, g, a, stream);
-}
+#ifndef TUNE_BLOCKS
+#define TUNE_BLOCKS 296
+#endif
 
 // channels per lane: bf16 pairs where every row starts on a pair (two channels fill a 32-bit
 // access), single channels otherwise
 cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, bool backward, cudaStream_t stream) {
-    if (s.io == 0) return launch_scan<float, 1>(s, a, backward, stream);
-    if (s.C % 2 == 0) return launch_scan<__nv_bfloat16, 2>(s, a, backward, stream);
-    return launch_scan<__nv_bfloat16, 1>(s, a, backward, stream);
+    if (s.io == 0) return launch_scan<float, 1, 8, 16, 0>(s, a, backward, stream);
+    if (s.C % 2 == 0) return launch_scan<__nv_bfloat16, 2, 8, 16, 0>(s, a, backward, stream);
+    return launch_scan<__nv_bfloat16, 1, 8, 16, 0>(s, a, backward, stream);
 }
 
 unsigned flat_blocks(int64_t units) {
