@@ -348,6 +348,8 @@ wkv_status eagle_decode_step(int64_t N, int64_t L, int64_t C, const float* w, co
  *              the state entering each 128 steps, which gated_scan_backward reads
  * T = 0 writes state_out only (state_in, or zeros).  One launch without a workspace; the sums
  * are taken in a fixed order, so equal calls give equal bits.
+ * A bounded device-side wait that gives up is recorded in the device-wide word that
+ * wkv_get_device_status reports (the outputs are then invalid).
  * Status codes as wkv_forward; WKV_ERR_UNSUPPORTED when B * ceil(C / 32) exceeds 2^28 - 1 (one
  * launch's blocks).
  */

@@ -3,18 +3,25 @@
 //
 // A span of steps maps the state entering it to the state leaving it by
 //   h_out = A h_in + H,   A = prod f_t,   H = the span's state from zero,
-// and two adjacent spans compose as (A1 A2, A2 H1 + H2), so the long axis is split: a warp
-// takes LC consecutive steps of 32 V adjacent channels into registers, sums them up as (A, H),
-// and once it knows the state entering its steps runs them again from the registers.  The
-// warps of a block cover a tile of kTile steps, the blocks of a cluster adjacent tiles; a
-// cluster walks its channels' sequence in strides of S tiles and carries the state from stride
-// to stride.  Summaries meet in (distributed) shared memory behind the hardware barriers, in a
+// and two adjacent spans compose as (A1 A2, A2 H1 + H2), so the long axis is split.  A warp
+// takes LC consecutive steps of 32 V adjacent channels and turns each token's gate and input
+// into the sums (A_t, H_t) of its steps so far; once it knows the state entering, every output
+// is one multiply-add.  The warps of a block cover a tile of adjacent steps, the blocks of a
+// cluster adjacent tiles; a cluster walks its channels' sequence in strides of S tiles and
+// carries the state from stride to stride.  Summaries meet in (distributed) shared memory, in a
 // fixed order: no workspace, no waiting on other clusters, and the same bits on every run.
+// Tiles are staged by TMA ahead of their use where the rows allow it.
 //
-// Arithmetic: fp32 whatever the I/O type.  A gate is kept as the smaller of (f, i) with the sign
-// of g, from e = 2^(-|g| log2 e) as e / (1 + e), relatively accurate at
-// both ends.  A step starts from whichever of h, x it stays near:
-//   i <= 1/2:  h + i (x - h)   where a gate holds for thousands of tokens f rounds to within
+// Bound by HBM: g and x are read once, y written once.  B200, forward (backward) against the
+// copy rate of 6549 GB/s: 1x16384x4096 fp32 118 us, 6830 GB/s (209 us, 6410 GB/s); 4x4096x2048
+// bf16 38.4 us, 5240 GB/s (78 us, 4270 GB/s); 8x1024x768 fp32 15.0 us, 5040 GB/s (25.3 us, 4970
+// GB/s).  In bf16 a byte carries twice the tokens and the issue slots are the limit (about 22
+// instructions per token forward, 35 backward).
+//
+// Arithmetic: fp32 whatever the I/O type.  A gate is kept as the smaller of (f, i) with a sign,
+// from e = 2^(-|g| log2 e) as e / (1 + e), relatively accurate at both ends.  A step starts from
+// whichever of h, x it stays near:
+//   i <= 1/2:  h - i (h - x)   where a gate holds for thousands of tokens f rounds to within
 //                              2^-24 of 1, and repeating f h would drift by that every step;
 //   f <  1/2:  x + f (h - x)   a closing gate leaves no rounding of the old state (f = 0: h = x).
 #include <cuda_bf16.h>
@@ -31,9 +38,7 @@
 namespace wkvb {
 namespace {
 
-constexpr int kTile = kGatedCarrySteps;   // steps per tile: one saved state each
-constexpr int kMaxCluster = 8;            // portable cluster size
-constexpr int kRowBytes = 128;            // one row of a staged tile
+constexpr int kMaxCluster = 8;  // portable cluster size
 
 struct ScanArgs {
     int64_t B, T, C;
@@ -48,6 +53,8 @@ struct ScanArgs {
     const float* gstate;     // backward: gradient of state_out, [B][C] or null
     uint32_t* dev_err;       // the library's device-wide error word
 };
+
+__device__ __forceinline__ int64_t saved_states(int64_t T) { return (T + kGatedCarrySteps - 1) / kGatedCarrySteps; }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -86,8 +93,6 @@ __device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a
 __device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float vmul(float a, float b) { return a * b; }
 __device__ __forceinline__ float2 vmul(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float vadd(float a, float b) { return a + b; }
-__device__ __forceinline__ float2 vadd(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float vsub(float a, float b) { return a - b; }
 __device__ __forceinline__ float2 vsub(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.f, -1.f), a); }
 
@@ -262,24 +267,26 @@ struct Block {
     }
     __device__ __forceinline__ T load_state(const float* p, int64_t row) const {
         float t[V];
+        if (p && live) {
+            Vec<float, V>::load(p + row * a.C + c, t);
+        } else {
 #pragma unroll
-        for (int q = 0; q < V; ++q) t[q] = p && live ? p[row * a.C + c + q] : 0.f;
+            for (int q = 0; q < V; ++q) t[q] = 0.f;
+        }
         return Lanes<V>::make(t);
     }
     __device__ __forceinline__ void store_state(float* p, int64_t row, T v) const {
         float t[V];
         Lanes<V>::split(v, t);
-        if (p && live)
-#pragma unroll
-            for (int q = 0; q < V; ++q) p[row * a.C + c + q] = t[q];
+        if (p && live) Vec<float, V>::store(p + row * a.C + c, t);
     }
     __device__ __forceinline__ void gave_up() const {
         atomicCAS(a.dev_err, kDevOk, (uint32_t)kDevTimeoutCopy);
     }
 };
 
-template <typename TIO, int V, int LC, int NW, int ST>
-__global__ void __launch_bounds__(32 * NW) scan_fwd(ScanArgs a, const __grid_constant__ CUtensorMap mg,
+template <typename TIO, int V, int LC, int NW, int ST, int MINB>
+__global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __grid_constant__ CUtensorMap mg,
                                                     const __grid_constant__ CUtensorMap mx) {
     using B = Block<TIO, V, LC, NW, ST, 2>;
     using T = typename B::T;
@@ -332,50 +339,55 @@ __global__ void __launch_bounds__(32 * NW) scan_fwd(ScanArgs a, const __grid_con
                 sg[s] = Lanes<V>::all(-0.f);
                 x[s] = Lanes<V>::all(0.f);
             }
+            // the two sums up to each token replace its gate and input: h_t = A_t h_in + H_t
             A = gate_decay(sg[s], A);
             H = gate_step(sg[s], H, x[s]);
+            sg[s] = A;
+            x[s] = H;
         }
         P(*ws)[32] = wsum[it & 1];
         ws[k.warp][k.lane] = Sp::pack(A, H);
         if (S > 1 && threadIdx.x == 0) ex.expect(it, S);
         __syncthreads();
         if (ST && threadIdx.x == 0 && j + (int64_t)ST * S < tiles) ring.fetch(it + ST, (j + (int64_t)ST * S) * k.tile, maps);
-        const int w0 = k.warp - k.wt;  // this warp's channels: warps w0 .. w0 + WT - 1 in time order
+        // this warp's channels: warps w0 .. w0 + WT - 1 in time order
+        const int w0 = ST ? 0 : k.warp - k.wt, WT = ST ? NW : k.WT;
         T h = carry;
         if (S > 1) {
-            if (k.wt == 0) {
-                T tA = Sp::A(ws[w0][k.lane]), tH = Sp::H(ws[w0][k.lane]);
-                for (int w = 1; w < k.WT; ++w) {
-                    const P p = ws[w0 + w][k.lane];
-                    tA = vmul(tA, Sp::A(p));
-                    tH = vfma(Sp::A(p), tH, Sp::H(p));
+            T tA = Lanes<V>::all(1.f), tH = Lanes<V>::all(0.f), pA = tA, pH = tH;
+#pragma unroll
+            for (int w = 0; w < WT; ++w) {
+                if (w == k.wt) {  // the block's steps before this warp's
+                    pA = tA;
+                    pH = tH;
                 }
-                ex.send(it, S, rank, k.lane, Sp::pack(tA, tH));
+                const P p = ws[w0 + w][k.lane];
+                tA = vmul(tA, Sp::A(p));
+                tH = vfma(Sp::A(p), tH, Sp::H(p));
             }
+            if (k.wt == 0) ex.send(it, S, rank, k.lane, Sp::pack(tA, tH));
             if (!ex.wait(it) && k.lane == 0) k.gave_up();
             for (uint32_t r = 0; r < S; ++r) {
                 if (r == rank) h = carry;
                 const P p = csum[it & 1][r][k.lane];
                 carry = vfma(Sp::A(p), carry, Sp::H(p));
             }
-            for (int w = 0; w < k.wt; ++w) {
-                const P p = ws[w0 + w][k.lane];
-                h = vfma(Sp::A(p), h, Sp::H(p));
-            }
+            h = vfma(pA, h, pH);
         } else {
-            for (int w = 0; w < k.WT; ++w) {
+#pragma unroll
+            for (int w = 0; w < WT; ++w) {
                 if (w == k.wt) h = carry;
                 const P p = ws[w0 + w][k.lane];
                 carry = vfma(Sp::A(p), carry, Sp::H(p));
             }
         }
-        if (a.carry && k.wt == 0 && j < tiles) k.store_state(a.carry, k.b * tiles + j, h);
+        if (a.carry && k.wt == 0 && j < tiles && t0 % kGatedCarrySteps == 0)
+            k.store_state(a.carry, k.b * saved_states(a.T) + t0 / kGatedCarrySteps, h);
         TIO* y = static_cast<TIO*>(a.y) + at;
 #pragma unroll
         for (int s = 0; s < LC; ++s) {
-            h = gate_step(sg[s], h, x[s]);
             float o[V];
-            Lanes<V>::split(h, o);
+            Lanes<V>::split(vfma(sg[s], h, x[s]), o);
             if (ALL || s < n) Vec<TIO, V>::store(y + s * a.C, o);
         }
     };
@@ -403,8 +415,8 @@ __global__ void __launch_bounds__(32 * NW) scan_fwd(ScanArgs a, const __grid_con
 // forward recurrence of the tile's own steps (the warps' H, exchanged together with M): g, x and
 // gy are read once and no other per-token value is needed.  m, lam and M are kept negated: every
 // product then is one of s with no sign change on a packed operand.
-template <typename TIO, int V, int LC, int NW, int ST>
-__global__ void __launch_bounds__(32 * NW) scan_bwd(ScanArgs a, const __grid_constant__ CUtensorMap mg,
+template <typename TIO, int V, int LC, int NW, int ST, int MINB>
+__global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __grid_constant__ CUtensorMap mg,
                                                     const __grid_constant__ CUtensorMap mx,
                                                     const __grid_constant__ CUtensorMap mgy) {
     using B = Block<TIO, V, LC, NW, ST, 3>;
@@ -444,7 +456,8 @@ __global__ void __launch_bounds__(32 * NW) scan_bwd(ScanArgs a, const __grid_con
     auto stride = [&](auto all, int64_t j, int64_t t0, int n) {
         constexpr bool ALL = decltype(all)::value;
         const int64_t at = (k.b * a.T + t0) * a.C + k.c;
-        T sg[LC], x[LC], gy[LC];
+        T sg[LC], x[LC], gy[LC], As[LC];
+        // a tile is kGatedCarrySteps long, or holds the whole sequence
         T h = j >= 0 ? k.load_state(a.carry, k.b * tiles + j) : Lanes<V>::all(0.f);
         if (ST) {
             load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 0) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, sg);
@@ -464,8 +477,12 @@ __global__ void __launch_bounds__(32 * NW) scan_bwd(ScanArgs a, const __grid_con
                 x[s] = Lanes<V>::all(0.f);
                 gy[s] = Lanes<V>::all(0.f);
             }
+            // x becomes h_{t-1} - x_t of the span from zero; the state entering adds As_t h_in to it
+            As[s] = A;
             A = gate_decay(sg[s], A);
-            H = gate_step(sg[s], H, x[s]);
+            const T d = vsub(H, x[s]);
+            H = vfma(sg[s], d, pick(sg[s], H, x[s]));
+            x[s] = d;
         }
 #pragma unroll
         for (int s = LC - 1; s >= 0; --s) M = gate_decay(sg[s], vsub(M, gy[s]));
@@ -476,40 +493,40 @@ __global__ void __launch_bounds__(32 * NW) scan_bwd(ScanArgs a, const __grid_con
         if (S > 1 && threadIdx.x == 0) ex.expect(it, S);
         __syncthreads();
         if (ST && threadIdx.x == 0 && j - (int64_t)ST * S >= 0) ring.fetch(it + ST, (j - (int64_t)ST * S) * k.tile, maps);
-        const int w0 = k.warp - k.wt;
+        const int w0 = ST ? 0 : k.warp - k.wt, WT = ST ? NW : k.WT;
+#pragma unroll
+        for (int w = 0; w < WT - 1; ++w)
+            if (w < k.wt) {
+                const P p = ws[w0 + w][k.lane];
+                h = vfma(Sp::A(p), h, Sp::H(p));
+            }
         T m = carry;
         if (S > 1) {
-            if (k.wt == 0) {
-                T tA = Lanes<V>::all(1.f), tM = Lanes<V>::all(0.f);
-                for (int w = k.WT - 1; w >= 0; --w) {
-                    const T wA = Sp::A(ws[w0 + w][k.lane]);
-                    tA = vmul(tA, wA);
-                    tM = vfma(wA, tM, wm[w0 + w][k.lane]);
+            T tA = Lanes<V>::all(1.f), tM = Lanes<V>::all(0.f), pA = tA, pM = tM;
+#pragma unroll
+            for (int w = WT - 1; w >= 0; --w) {
+                if (w == k.wt) {  // the block's steps after this warp's
+                    pA = tA;
+                    pM = tM;
                 }
-                ex.send(it, S, rank, k.lane, Sp::pack(tA, tM));
+                const T wA = Sp::A(ws[w0 + w][k.lane]);
+                tA = vmul(tA, wA);
+                tM = vfma(wA, tM, wm[w0 + w][k.lane]);
             }
+            if (k.wt == 0) ex.send(it, S, rank, k.lane, Sp::pack(tA, tM));
             if (!ex.wait(it) && k.lane == 0) k.gave_up();
             for (uint32_t r = 0; r < S; ++r) {
                 if (r == rank) m = carry;
                 const P p = csum[it & 1][r][k.lane];
                 carry = vfma(Sp::A(p), carry, Sp::H(p));
             }
-            for (int w = k.WT - 1; w > k.wt; --w) m = vfma(Sp::A(ws[w0 + w][k.lane]), m, wm[w0 + w][k.lane]);
+            m = vfma(pA, m, pM);
         } else {
-            for (int w = k.WT - 1; w >= 0; --w) {
+#pragma unroll
+            for (int w = WT - 1; w >= 0; --w) {
                 if (w == k.wt) m = carry;
                 carry = vfma(Sp::A(ws[w0 + w][k.lane]), carry, wm[w0 + w][k.lane]);
             }
-        }
-        for (int w = 0; w < k.wt; ++w) {
-            const P p = ws[w0 + w][k.lane];
-            h = vfma(Sp::A(p), h, Sp::H(p));
-        }
-#pragma unroll
-        for (int s = 0; s < LC; ++s) {  // x becomes f i (x_t - h_{t-1})
-            const T d = vsub(h, x[s]);
-            h = vfma(sg[s], d, pick(sg[s], h, x[s]));
-            x[s] = vmul(gate_slope_neg(sg[s]), d);
         }
         TIO* gx = static_cast<TIO*>(a.y) + at;
         TIO* gg = static_cast<TIO*>(a.gg) + at;
@@ -518,7 +535,7 @@ __global__ void __launch_bounds__(32 * NW) scan_bwd(ScanArgs a, const __grid_con
             const T lam = vsub(m, gy[s]);  // negated, as m
             float ox[V], og[V];
             Lanes<V>::split(gate_input_neg(sg[s], lam), ox);
-            Lanes<V>::split(vmul(x[s], lam), og);
+            Lanes<V>::split(vmul(vmul(gate_slope_neg(sg[s]), vfma(As[s], h, x[s])), lam), og);
             m = gate_decay(sg[s], lam);
             if (ALL || s < n) {
                 Vec<TIO, V>::store(gx + s * a.C, ox);
@@ -570,77 +587,107 @@ __global__ void copy_or_zero(int64_t n, const float* in, float* out) {
         out[i] = in ? in[i] : 0.f;
 }
 
-struct ScanGeom {
-    int wt_log, S;
-    int64_t groups, blocks;
-};
-
 int sm_count() {
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     return sms;
 }
 
-ScanGeom scan_geometry(const GatedScanShape& s, int V, int LC, int NW, int most_blocks) {
-    ScanGeom g;
-    g.wt_log = 0;
-    while ((1 << g.wt_log) < NW && (int64_t)(LC << g.wt_log) < s.T) ++g.wt_log;
-    const int64_t W = (int64_t)(NW >> g.wt_log) * 32 * V;
-    g.groups = (s.C + W - 1) / W;
-    const int64_t units = s.B * g.groups, tiles = (s.T + LC * NW - 1) / (LC * NW);
-    g.S = 1;
-    while (g.S < kMaxCluster && g.S < tiles && units * g.S * 2 <= most_blocks) g.S *= 2;
-    g.blocks = units * g.S;
-    return g;
-}
+// One configuration: V channels per lane, LC steps per warp, NW warps per block, ST staged tiles,
+// RES blocks resident per SM.  S, the blocks of a cluster, doubles while every block is resident.
+template <typename TIO, int V, int LC, int NW, int ST, int RES, bool BWD>
+cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream) {
+    constexpr int kArrays = BWD ? 3 : 2, kSmem = ST * kArrays * LC * NW * 32 * V * (int)sizeof(TIO);
+    while ((1 << a.wt_log) < NW && (ST || (int64_t)(LC << a.wt_log) < s.T)) ++a.wt_log;
+    const int64_t W = (int64_t)(NW >> a.wt_log) * 32 * V, tiles = (s.T + LC * NW - 1) / (LC * NW);
+    a.groups = (s.C + W - 1) / W;
+    const int64_t units = s.B * a.groups, room = (int64_t)sm_count() * RES;
+    int S = 1;
+    while (S < kMaxCluster && S < tiles && units * S * 2 <= room) S *= 2;
 
-template <typename TIO, int V, int LC, int NW, int ST>
-cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, bool backward, cudaStream_t stream) {
-    const int arrays = backward ? 3 : 2;
-    const int smem = ST * arrays * LC * NW * 32 * V * (int)sizeof(TIO);
-    ScanGeom g = scan_geometry(s, V, LC, NW, TUNE_BLOCKS);
-    a.groups = g.groups;
-    a.wt_log = g.wt_log;
     CUtensorMap m[3] = {};
     if (ST) {
         const void* from[3] = {a.g, a.x, a.gy};
-        g.wt_log = 0;
-        for (int k = 0; k < arrays; ++k)
-            if (!make_tile_map(&m[k], from[k], s.B, s.T, s.C, s.io, 32 * V, LC * NW))
-                return cudaErrorInvalidValue;
+        for (int k = 0; k < kArrays; ++k)
+            if (!make_tile_map(&m[k], from[k], s.B, s.T, s.C, s.io, 32 * V, LC * NW)) return cudaErrorInvalidValue;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)g.blocks);
+    cfg.gridDim = dim3((unsigned)(units * S));
     cfg.blockDim = dim3(32 * NW);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch ? 1 : 0;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim = {(unsigned)g.S, 1, 1};
+    at[1].val.clusterDim = {(unsigned)S, 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    if (backward) {
-        auto kern = scan_bwd<TIO, V, LC, NW, ST>;
-        if (smem) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if constexpr (BWD) {
+        auto kern = scan_bwd<TIO, V, LC, NW, ST, RES>;
+        if (kSmem > 0)
+            if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
         return cudaLaunchKernelEx(&cfg, kern, a, m[0], m[1], m[2]);
+    } else {
+        auto kern = scan_fwd<TIO, V, LC, NW, ST, RES>;
+        if (kSmem > 0)
+            if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
+        return cudaLaunchKernelEx(&cfg, kern, a, m[0], m[1]);
     }
-    auto kern = scan_fwd<TIO, V, LC, NW, ST>;
-    if (smem) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return cudaLaunchKernelEx(&cfg, kern, a, m[0], m[1]);
 }
 
-#ifndef TUNE_BLOCKS
-#define TUNE_BLOCKS 296
-#endif
+// Times below: us on a B200 in a CUDA graph, inputs over the L2, shapes B x T x C.
+//
+// Staged tiles, for rows of a multiple of 16 bytes and sequences of more than kShort steps:
+// 64x32x2048 fp32 takes 33 staged and 13 direct (a short tile leaves warps idle), 32x128x2048 20
+// and 21, 8x1024x768 15 and 26.
+constexpr int64_t kShort = 64;
 
-// channels per lane: bf16 pairs where every row starts on a pair (two channels fill a 32-bit
-// access), single channels otherwise
-cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, bool backward, cudaStream_t stream) {
-    if (s.io == 0) return launch_scan<float, 1, 8, 16, 0>(s, a, backward, stream);
-    if (s.C % 2 == 0) return launch_scan<__nv_bfloat16, 2, 8, 16, 0>(s, a, backward, stream);
-    return launch_scan<__nv_bfloat16, 1, 8, 16, 0>(s, a, backward, stream);
+bool staged_rows(const GatedScanShape& s) {
+    const int64_t es = s.io == 1 ? 2 : 4;
+    return s.T > kShort && s.C * es % 16 == 0 && s.T <= INT32_MAX && s.C <= INT32_MAX &&
+           s.T * s.C * es < (int64_t(1) << 40);  // a tensor map's stride
+}
+
+// Pairs per lane halve the instructions, single channels make twice the blocks.  Pairs win where
+// even single channels leave the SMs to a few long sequences (1x16384x4096 fp32: forward 118
+// against 143, backward 209 against 257), single channels elsewhere (8x1024x768: 15.0 against
+// 16.3, 25.3 against 26.7).
+bool wide_lanes(const GatedScanShape& s) {
+    return s.B * ((s.C + 31) / 32) < 2 * (int64_t)sm_count() && s.T >= 32 * kGatedCarrySteps;
+}
+
+// Direct: the lanes read global memory.  Any row; a warp's steps no longer than the sequence
+// needs (512x1x4096 fp32 with 8 steps per warp: 38).  The backward's tile holds the sequence, or
+// one saved state's steps.
+template <typename TIO, int V, bool BWD>
+cudaError_t launch_direct(const GatedScanShape& s, const ScanArgs& a, cudaStream_t stream) {
+    if (s.T == 1) return launch_scan<TIO, V, 1, 4, 0, 4, BWD>(s, a, stream);
+    if (s.T <= 4) return launch_scan<TIO, V, 4, 4, 0, 4, BWD>(s, a, stream);
+    if (s.T <= 32) return launch_scan<TIO, V, 8, 4, 0, 4, BWD>(s, a, stream);
+    if (s.T <= 64) return launch_scan<TIO, V, 8, 8, 0, 2, BWD>(s, a, stream);
+    return launch_scan<TIO, V, 16, 8, 0, 1, BWD>(s, a, stream);
+}
+
+// The forward's staged form: 32 steps per warp and four warps (fewer summaries to fold: bf16
+// 4x4096x2048 38 against 43 with 16 steps and eight warps); bf16 always in pairs (a row of the
+// tile is then 128 bytes: 4x4096x2048 38 against 54).  The backward holds four values per token,
+// which 32 steps spill: 16 steps, eight warps.
+template <typename TIO, bool BWD>
+cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t stream) {
+    constexpr bool kHalf = sizeof(TIO) == 2;
+    if (staged_rows(s)) {
+        if constexpr (BWD) {
+            if (wide_lanes(s)) return launch_scan<TIO, 2, 16, 8, 2, 1, true>(s, a, stream);
+            return launch_scan<TIO, 1, 16, 8, 2, 2, true>(s, a, stream);
+        } else if constexpr (kHalf) {
+            return launch_scan<TIO, 2, 32, 4, 2, 2, false>(s, a, stream);
+        } else {
+            if (wide_lanes(s)) return launch_scan<TIO, 2, 32, 4, 2, 1, false>(s, a, stream);
+            return launch_scan<TIO, 1, 32, 4, 2, 3, false>(s, a, stream);
+        }
+    }
+    return s.C % 2 == 0 ? launch_direct<TIO, 2, BWD>(s, a, stream) : launch_direct<TIO, 1, BWD>(s, a, stream);
 }
 
 unsigned flat_blocks(int64_t units) {
@@ -671,7 +718,9 @@ cudaError_t launch_gated_scan_forward(const GatedScanShape& s, const void* g, co
     a.y = y;
     a.state_out = state_out;
     a.carry = carry;
-    return dispatch_scan(s, a, false, stream);
+    a.dev_err = device_status_word();
+    if (!a.dev_err) return cudaGetLastError();
+    return s.io == 1 ? dispatch_scan<__nv_bfloat16, false>(s, a, stream) : dispatch_scan<float, false>(s, a, stream);
 }
 
 cudaError_t launch_gated_scan_backward(const GatedScanShape& s, const void* g, const void* x, const float* carry,
@@ -693,7 +742,9 @@ cudaError_t launch_gated_scan_backward(const GatedScanShape& s, const void* g, c
     a.gg = gg;
     a.state_out = gstate_in;
     a.carry = const_cast<float*>(carry);
-    return dispatch_scan(s, a, true, stream);
+    a.dev_err = device_status_word();
+    if (!a.dev_err) return cudaGetLastError();
+    return s.io == 1 ? dispatch_scan<__nv_bfloat16, true>(s, a, stream) : dispatch_scan<float, true>(s, a, stream);
 }
 
 cudaError_t launch_gated_scan_step(int64_t n, int io, const void* g, const void* x, float* state, void* y,
