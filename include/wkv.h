@@ -386,6 +386,57 @@ wkv_status gated_scan_backward(int64_t B, int64_t T, int64_t C, wkv_dtype io, co
 wkv_status gated_scan_step(int64_t N, int64_t L, int64_t C, wkv_dtype io, const void* g, const void* x,
                            float* state_inout, void* y, cudaStream_t stream);
 
+typedef enum wkv_act {
+    WKV_ACT_NONE = 0,    /* act(v) = v */
+    WKV_ACT_SILU = 1,    /* act(v) = v sigma(v) */
+    WKV_ACT_SIGMOID = 2  /* act(v) = sigma(v) */
+} wkv_act;
+
+/*
+ * Gated group norm over the channels of each row, channels last: the per-head normalisation and
+ * gate that read out a matrix-state or gated recurrence (eagle_forward's and gated_scan_forward's
+ * y).  A row's C channels are `groups` groups of D = C / groups adjacent ones (Eagle: 64); per
+ * row and group
+ *
+ *   n = (x - mean x) / sqrt(mean((x - mean x)^2) + eps),   a = n weight + bias
+ *   y = a act(z) with a gate z,   y = act(a) without
+ *
+ *   rows          B * T, or N * L for single tokens
+ *   x, z, y       [rows, C] in dtype io (z may be NULL: no gate; y written, must not overlap)
+ *   weight, bias  [C] fp32, or NULL for 1 and 0
+ *   eps           >= 0 and finite (0 with a group of equal values divides by zero)
+ * groups must divide C (else WKV_ERR_INVALID_ARG).  Statistics and arithmetic are fp32 for both
+ * I/O types, the variance taken about the mean; a value not finite, or whose square is not, makes
+ * its own row's group non-finite or meaningless and touches no other.  Any D; D a multiple of 4
+ * (fp32) or 8 (bf16) takes 16-byte accesses.  One launch, no workspace.  Status codes as wkv_forward;
+ * WKV_ERR_UNSUPPORTED for an unknown act, or C above 2^31 - 1.
+ */
+wkv_status group_norm_gated(int64_t rows, int64_t C, int64_t groups, wkv_dtype io, float eps, wkv_act act,
+                            const void* x, const void* z, const float* weight, const float* bias, void* y,
+                            cudaStream_t stream);
+
+/*
+ * Its gradients for a loss L with gy = dL/dy (the statistics are taken again from x):
+ *   with a gate   gz = gy a act'(z),  ga = gy act(z);   without   ga = gy act'(a)
+ *   gbias = sum over rows of ga,  gweight = sum over rows of ga n,  gn = ga weight
+ *   gx = (gn - mean gn - n mean(gn n)) / sqrt(var + eps)   (means over the row's group)
+ *   x, z, gy, gx, gz  [rows, C] in dtype io (gx, gz written; gz required with z, else NULL)
+ *   gweight, gbias    [C] fp32 (written), or NULL
+ *   workspace         caller-owned scratch of ws_bytes >= group_norm_gated_backward_workspace_size(),
+ *                     no initial contents needed, NULL when neither gweight nor gbias is wanted; one
+ *                     workspace must not serve two calls that can run at the same time
+ * rows = 0 writes zeros to gweight and gbias.  The sums over rows are taken in a fixed order (equal
+ * calls give equal bits).  Status codes as group_norm_gated.
+ */
+wkv_status group_norm_gated_backward(int64_t rows, int64_t C, int64_t groups, wkv_dtype io, float eps, wkv_act act,
+                                     const void* x, const void* z, const float* weight, const float* bias,
+                                     const void* gy, void* gx, void* gz, float* gweight, float* gbias,
+                                     void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes group_norm_gated_backward needs for gweight and gbias: 8 per channel and block
+ * of rows (at most 1184 blocks); 0 for an invalid or empty shape.  No device call. */
+size_t group_norm_gated_backward_workspace_size(int64_t rows, int64_t C, int64_t groups, wkv_dtype io);
+
 /* Human-readable name of a status code (static string). */
 const char* wkv_status_string(wkv_status status);
 

@@ -20,6 +20,9 @@ Entry points (same names as the C ABI):
   ``(y, state_out, carry)``, ``gated_scan_backward(g, x, carry, gy, gstate_out=None)`` ->
   ``(gg, gx, gstate_in)`` and ``gated_scan_step(g, x, state)`` -> ``y``: the gated linear
   recurrence, its gradients and one token of it (fp32 or bf16).
+* ``group_norm_gated(x, z=None, weight=None, bias=None, groups=1, eps=1e-5, act="silu")`` ->
+  ``y`` and ``group_norm_gated_backward(x, z, weight, bias, gy, ...)`` ->
+  ``(gx, gz, gweight, gbias)``: the per-head normalisation and gate of a read-out.
 """
 from __future__ import annotations
 
@@ -33,7 +36,7 @@ from . import build as _build
 
 __all__ = [
     "WkvError", "Workspace", "wkv_forward", "wkv_decode_step", "wkv_decode_step_fused", "token_shift_mix",
-    "gated_scan_forward", "gated_scan_backward", "gated_scan_step",
+    "gated_scan_forward", "gated_scan_backward", "gated_scan_step", "group_norm_gated", "group_norm_gated_backward",
     "workspace_size", "forward_status", "auto_path", "lib", "LIB_PATH", "STATUS",
 ]
 
@@ -41,6 +44,7 @@ LIB_PATH = _build.LIB_PATH
 STATUS = {0: "WKV_OK", 1: "WKV_ERR_INVALID_ARG", 2: "WKV_ERR_MISALIGNED", 3: "WKV_ERR_UNSUPPORTED",
           4: "WKV_ERR_CUDA", 5: "WKV_ERR_TIMEOUT"}
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+_ACT = {"none": 0, "silu": 1, "sigmoid": 2}
 _PATH = {"auto": 0, "serial": 1, "chunked": 2}
 
 
@@ -90,6 +94,11 @@ def lib():
                 L.gated_scan_step.argtypes = [i64, i64, i64, i32] + [vp] * 5
                 L.gated_scan_carry_size.argtypes = [i64, i64, i64]
                 L.gated_scan_carry_size.restype = sz
+                f32 = ctypes.c_float
+                L.group_norm_gated.argtypes = [i64, i64, i64, i32, f32, i32] + [vp] * 6
+                L.group_norm_gated_backward.argtypes = [i64, i64, i64, i32, f32, i32] + [vp] * 10 + [sz, vp]
+                L.group_norm_gated_backward_workspace_size.argtypes = [i64, i64, i64, i32]
+                L.group_norm_gated_backward_workspace_size.restype = sz
                 L.wkv_status_string.argtypes = [i32]
                 L.wkv_status_string.restype = ctypes.c_char_p
                 L.wkv_forward_auto_path.argtypes = [i64, i64, i64, i32]
@@ -98,7 +107,8 @@ def lib():
                           L.wkv_get_device_status, L.wkv_forward_gated, L.token_shift_mix3, L.wkv_backward,
                           L.wkv_decode_step, L.wkv_decode_step_fused, L.token_shift_mix,
                           L.wkv_forward_auto_path, L.wkv_testhook_forward_drop, L.gated_scan_forward,
-                          L.gated_scan_backward, L.gated_scan_step):
+                          L.gated_scan_backward, L.gated_scan_step, L.group_norm_gated,
+                          L.group_norm_gated_backward):
                     f.restype = i32
                 _lib = L
     return _lib
@@ -454,3 +464,58 @@ def gated_scan_step(g, x, state, y=None):
     _launch(lib().gated_scan_step, (g, x, state, y), N, L, C, _DTYPE[g.dtype], g.data_ptr(), x.data_ptr(),
             state.data_ptr(), y.data_ptr())
     return y
+
+
+def _norm_args(x, z, weight, bias, groups, act):
+    _io(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have a channel dimension")
+    if z is not None:
+        _io(z, "z", like=x)
+    C = x.shape[-1]
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _cuda_f32(t, name, (C,))
+    if groups < 1 or C % groups:
+        raise ValueError(f"groups = {groups} must divide the {C} channels")
+    if act not in _ACT:
+        raise ValueError(f"act must be one of {sorted(_ACT)}, got {act!r}")
+    return x.numel() // C if C else 0, C
+
+
+def group_norm_gated(x, z=None, weight=None, bias=None, groups=1, eps=1e-5, act="silu", y=None):
+    """Group norm over the last dimension of x (`groups` groups of adjacent channels per row), scaled
+    by weight and shifted by bias ([C] fp32, None: 1 and 0), then gated: y = a act(z), or act(a)
+    without z.  z has x's shape; act is "none", "silu" or "sigmoid".  Returns y."""
+    rows, C = _norm_args(x, z, weight, bias, groups, act)
+    y = torch.empty_like(x) if y is None else _io(y, "y", like=x)
+    _launch(lib().group_norm_gated, (x, z, weight, bias, y), rows, C, groups, _DTYPE[x.dtype], eps, _ACT[act],
+            x.data_ptr(), _ptr(z), _ptr(weight), _ptr(bias), y.data_ptr())
+    return y
+
+
+def group_norm_gated_backward(x, z, weight, bias, gy, groups=1, eps=1e-5, act="silu", want_params=True, gx=None,
+                              gz=None, workspace=None):
+    """Gradients of group_norm_gated given gy: returns (gx, gz, gweight, gbias); gz is None without a
+    gate, gweight and gbias ([C] fp32) are None unless want_params.  A workspace passed in needs no
+    initial contents and must be reused only in order."""
+    rows, C = _norm_args(x, z, weight, bias, groups, act)
+    _io(gy, "gy", like=x)
+    gx = torch.empty_like(x) if gx is None else _io(gx, "gx", like=x)
+    if z is None:
+        if gz is not None:
+            raise ValueError("gz without z")
+    else:
+        gz = torch.empty_like(x) if gz is None else _io(gz, "gz", like=x)
+    gweight = gbias = ws = None
+    if want_params:
+        both = torch.empty((2, (C + 3) // 4 * 4), dtype=torch.float32, device=x.device)
+        gweight, gbias = both[0, :C], both[1, :C]
+        nbytes = int(lib().group_norm_gated_backward_workspace_size(rows, C, groups, _DTYPE[x.dtype]))
+        ws = workspace if workspace is not None and workspace.numel() * workspace.element_size() >= nbytes else \
+            torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+    _launch(lib().group_norm_gated_backward, (x, z, weight, bias, gy, gx, gz, gweight, ws), rows, C, groups,
+            _DTYPE[x.dtype], eps, _ACT[act], x.data_ptr(), _ptr(z), _ptr(weight), _ptr(bias), gy.data_ptr(),
+            gx.data_ptr(), _ptr(gz), _ptr(gweight), _ptr(gbias), _ptr(ws),
+            0 if ws is None else ws.numel() * ws.element_size())
+    return gx, gz, gweight, gbias

@@ -7,10 +7,12 @@ shares one runtime instance with PyTorch in the same process.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -53,15 +55,23 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if not force and up_to_date():
         return LIB_PATH
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc()] + NVCC_FLAGS + ["-I", INCLUDE, "-I", CSRC] + (["-Xptxas", "-v"] if ptxas_info else []) + \
-        sources() + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
-    if verbose or ptxas_info:
-        print(res.stdout + res.stderr, file=sys.stderr)
+    common = [nvcc()] + NVCC_FLAGS + ["-I", INCLUDE, "-I", CSRC]
+    # the sources compile side by side, then one link
+    with tempfile.TemporaryDirectory() as objs:
+        steps = [common + (["-Xptxas", "-v"] if ptxas_info else []) +
+                 ["-c", src, "-o", os.path.join(objs, os.path.basename(src) + ".o")] for src in sources()]
+        with concurrent.futures.ThreadPoolExecutor(os.cpu_count()) as pool:
+            done = list(pool.map(lambda cmd: (cmd, subprocess.run(cmd, capture_output=True, text=True)), steps))
+        if all(res.returncode == 0 for _, res in done):
+            link = common + [cmd[-1] for cmd in steps] + ["-o", tmp]
+            done.append((link, subprocess.run(link, capture_output=True, text=True)))
+    for cmd, res in done:
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        if res.returncode != 0:
+            raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        if verbose or ptxas_info:
+            print(res.stdout + res.stderr, file=sys.stderr)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -346,6 +346,62 @@ wkv_status gated_scan_step(int64_t N, int64_t L, int64_t C, wkv_dtype io, const 
     return e == cudaSuccess ? WKV_OK : cuda_fail(e);
 }
 
+namespace {
+
+// The checks the group norm's calls share: WKV_OK with a shape to run, or the refusal; an empty
+// call (no channels) is reported through `empty`.
+wkv_status norm_shape(int64_t rows, int64_t C, int64_t groups, wkv_dtype io, float eps, wkv_act act, GroupNormShape* s,
+                      bool* empty) {
+    int64_t n = 0;
+    if (!mul_ok(rows, C, &n) || n > INT64_MAX / 64) return WKV_ERR_INVALID_ARG;
+    if (io != WKV_F32 && io != WKV_BF16) return WKV_ERR_UNSUPPORTED;
+    if (act != WKV_ACT_NONE && act != WKV_ACT_SILU && act != WKV_ACT_SIGMOID) return WKV_ERR_UNSUPPORTED;
+    if (groups < 1 || C % groups != 0 || !(eps >= 0.f) || std::isinf(eps)) return WKV_ERR_INVALID_ARG;
+    if (C > INT32_MAX) return WKV_ERR_UNSUPPORTED;
+    *empty = C == 0;
+    *s = GroupNormShape{rows, C, groups, (int)io, eps, (int)act};
+    return WKV_OK;
+}
+
+}  // namespace
+
+wkv_status group_norm_gated(int64_t rows, int64_t C, int64_t groups, wkv_dtype io, float eps, wkv_act act,
+                            const void* x, const void* z, const float* weight, const float* bias, void* y,
+                            cudaStream_t stream) {
+    GroupNormShape s;
+    bool empty;
+    if (wkv_status st = norm_shape(rows, C, groups, io, eps, act, &s, &empty)) return st;
+    if (empty || rows == 0) return WKV_OK;
+    if (!x || !y) return WKV_ERR_INVALID_ARG;
+    if (!f32_args_ok({x, z, weight, bias, y})) return WKV_ERR_MISALIGNED;
+    cudaError_t e = launch_group_norm_forward(s, x, z, weight, bias, y, stream);
+    return e == cudaSuccess ? WKV_OK : cuda_fail(e);
+}
+
+size_t group_norm_gated_backward_workspace_size(int64_t rows, int64_t C, int64_t groups, wkv_dtype io) {
+    GroupNormShape s;
+    bool empty;
+    if (norm_shape(rows, C, groups, io, 0.f, WKV_ACT_NONE, &s, &empty) || empty || rows == 0) return 0;
+    return group_norm_workspace_bytes(s);
+}
+
+wkv_status group_norm_gated_backward(int64_t rows, int64_t C, int64_t groups, wkv_dtype io, float eps, wkv_act act,
+                                     const void* x, const void* z, const float* weight, const float* bias,
+                                     const void* gy, void* gx, void* gz, float* gweight, float* gbias,
+                                     void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    GroupNormShape s;
+    bool empty;
+    if (wkv_status st = norm_shape(rows, C, groups, io, eps, act, &s, &empty)) return st;
+    if (empty) return WKV_OK;
+    if (rows > 0 && (!x || !gy || !gx || (z && !gz) || (!z && gz))) return WKV_ERR_INVALID_ARG;
+    if (!f32_args_ok({x, z, weight, bias, gy, gx, gz, gweight, gbias, workspace})) return WKV_ERR_MISALIGNED;
+    if (rows == 0 && !gweight && !gbias) return WKV_OK;
+    if (rows > 0 && (gweight || gbias) && (!workspace || ws_bytes < group_norm_workspace_bytes(s)))
+        return WKV_ERR_INVALID_ARG;
+    cudaError_t e = launch_group_norm_backward(s, x, z, weight, bias, gy, gx, gz, gweight, gbias, workspace, stream);
+    return e == cudaSuccess ? WKV_OK : cuda_fail(e);
+}
+
 wkv_status wkv_forward_status(void* workspace, size_t ws_bytes, cudaStream_t stream) {
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(e);

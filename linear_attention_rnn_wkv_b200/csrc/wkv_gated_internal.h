@@ -27,4 +27,23 @@ cudaError_t launch_gated_scan_backward(const GatedScanShape& s, const void* g, c
 cudaError_t launch_gated_scan_step(int64_t n, int io, const void* g, const void* x, float* state, void* y,
                                    cudaStream_t s);
 
+// Activations of the group norm (the C ABI's wkv_act).
+enum : int { kActNone = 0, kActSilu = 1, kActSigmoid = 2 };
+
+struct GroupNormShape {
+    int64_t rows, C, groups;
+    int io;  // 0 fp32, 1 bf16
+    float eps;
+    int act;
+};
+
+// Scratch of the backward's weight and bias sums.
+size_t group_norm_workspace_bytes(const GroupNormShape& s);
+cudaError_t launch_group_norm_forward(const GroupNormShape& s, const void* x, const void* z, const float* weight,
+                                      const float* bias, void* y, cudaStream_t stream);
+// workspace may be null when neither gweight nor gbias is wanted
+cudaError_t launch_group_norm_backward(const GroupNormShape& s, const void* x, const void* z, const float* weight,
+                                       const float* bias, const void* gy, void* gx, void* gz, float* gweight, float* gbias,
+                                       void* workspace, cudaStream_t stream);
+
 }  // namespace wkvb

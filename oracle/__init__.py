@@ -35,6 +35,10 @@ Functions (all inputs are converted to contiguous float64):
   ``h_t = sigma(g_t) h_{t-1} + sigma(-g_t) x_t``.  Returns ``(y, s, state_out, s_out)``.
 * ``gated_scan_backward(g, x, gy, state_in=None, gstate_out=None)`` -- its gradients.
   Returns ``(gg, gx, gstate_in, (sg, sx, ss))``.
+* ``group_norm_gated(x, z, weight, bias, groups, eps, act)`` -- group norm of each row's
+  channels, gated.  Returns ``(y, s)``.
+* ``group_norm_gated_backward(x, z, weight, bias, gy, groups, eps, act)`` -- its gradients.
+  Returns ``(gx, gz, gweight, gbias, (sx, sz, sw, sb))`` (gz, sz None without z).
 
 ``s`` is the same weighted average with ``|v|`` in place of ``v`` (the error
 scale the parity tests divide by); ``sacc`` is its accumulator in the state.
@@ -82,7 +86,10 @@ def load(path: str):
     L.oracle_eagle_direct.argtypes = [i64, i64, i64, i64] + [vp] * 6
     L.oracle_gated_scan.argtypes = [i64, i64, i64] + [vp] * 7
     L.oracle_gated_scan_backward.argtypes = [i64, i64, i64] + [vp] * 13
-    for f in (L.oracle_gated_scan, L.oracle_gated_scan_backward, L.oracle_wkv_direct, L.oracle_wkv_recurrent, L.oracle_wkv_naive, L.oracle_token_shift, L.oracle_gate,
+    dbl = ctypes.c_double
+    L.oracle_group_norm_gated.argtypes = [i64, i64, i64, dbl, ctypes.c_int] + [vp] * 6
+    L.oracle_group_norm_gated_backward.argtypes = [i64, i64, i64, dbl, ctypes.c_int] + [vp] * 13
+    for f in (L.oracle_group_norm_gated, L.oracle_group_norm_gated_backward, L.oracle_gated_scan, L.oracle_gated_scan_backward, L.oracle_wkv_direct, L.oracle_wkv_recurrent, L.oracle_wkv_naive, L.oracle_token_shift, L.oracle_gate,
               L.oracle_wkv_backward_direct, L.oracle_eagle_recurrent, L.oracle_eagle_direct):
         f.restype = None
     L.oracle_num_threads.restype = ctypes.c_int
@@ -263,3 +270,33 @@ def gated_scan_backward(g, x, gy, state_in=None, gstate_out=None, L=None):
     (L or lib()).oracle_gated_scan_backward(B, T, C, _p(g), _p(x), _p(state_in), _p(y), _p(s), _p(gy),
                                             _p(gstate_out), _p(gg), _p(gx), _p(gs), _p(sg), _p(sx), _p(ss))
     return gg, gx, gs, (sg, sx, ss)
+
+
+_ACT = {"none": 0, "silu": 1, "sigmoid": 2}
+
+
+def _norm_shape(x, z, weight, bias, groups):
+    C = x.shape[-1]
+    if C % groups:
+        raise ValueError(f"{groups} groups do not divide {C} channels")
+    return (x.size // C, groups, C // groups) + tuple(None if a is None else _f64(a) for a in (z, weight, bias))
+
+
+def group_norm_gated(x, z, weight, bias, groups, eps, act, L=None):
+    x = _f64(x)
+    rows, G, D, z, weight, bias = _norm_shape(x, z, weight, bias, groups)
+    y, s = np.empty(x.shape), np.empty(x.shape)
+    (L or lib()).oracle_group_norm_gated(rows, G, D, eps, _ACT[act], _p(x), _p(z), _p(weight), _p(bias), _p(y), _p(s))
+    return y, s
+
+
+def group_norm_gated_backward(x, z, weight, bias, gy, groups, eps, act, L=None):
+    x, gy = _f64(x), _f64(gy)
+    rows, G, D, z, weight, bias = _norm_shape(x, z, weight, bias, groups)
+    gx, sx = np.empty(x.shape), np.empty(x.shape)
+    gz, sz = (None, None) if z is None else (np.empty(x.shape), np.empty(x.shape))
+    gw, gb, sw, sb = (np.empty(G * D) for _ in range(4))
+    (L or lib()).oracle_group_norm_gated_backward(rows, G, D, eps, _ACT[act], _p(x), _p(z), _p(weight), _p(bias),
+                                                  _p(gy), _p(gx), _p(gz), _p(gw), _p(gb), _p(sx), _p(sz), _p(sw),
+                                                  _p(sb))
+    return gx, gz, gw, gb, (sx, sz, sw, sb)

@@ -466,3 +466,119 @@ void oracle_gated_scan_backward(int64_t B, int64_t T, int64_t C, const double* g
             ss[b * C + c] = ms;
         }
 }
+
+/*
+ * Gated group norm over each row's C = G * D channels.  act: 0 none, 1 SiLU, 2 sigma; z, weight,
+ * bias may be NULL (no gate; 1; 0).  Per row and group of D adjacent channels
+ *   n = (x - mean) / sqrt(var + eps), var about the mean;  a = n weight + bias;
+ *   y = a act(z), or act(a) without z.
+ * s: the magnitude scale of y, with sn = max|x| / sqrt(var + eps) + |n| in place of |n| (the
+ * difference x - mean carries the rounding of the group's largest value):
+ *   sa = |weight| sn + |bias|;  s = sa |act(z)|, or 1.1 sa + |act(a)| (|act'| <= 1.1).
+ */
+static double oracle_act(int act, double v)
+{
+    const double p = 1.0 / (1.0 + exp(-v));
+    return act == 0 ? v : act == 1 ? v * p : p;
+}
+
+static void oracle_norm_row(int64_t D, double eps, const double* x, double* n, double* sn, double* rstd)
+{
+    double mean = 0.0, var = 0.0, top = 0.0;
+    for (int64_t i = 0; i < D; ++i) mean += x[i];
+    mean /= (double)D;
+    for (int64_t i = 0; i < D; ++i) {
+        var += (x[i] - mean) * (x[i] - mean);
+        if (fabs(x[i]) > top) top = fabs(x[i]);
+    }
+    *rstd = 1.0 / sqrt(var / (double)D + eps);
+    for (int64_t i = 0; i < D; ++i) {
+        n[i] = (x[i] - mean) * *rstd;
+        sn[i] = top * *rstd + fabs(n[i]);
+    }
+}
+
+void oracle_group_norm_gated(int64_t rows, int64_t G, int64_t D, double eps, int act, const double* x,
+                             const double* z, const double* weight, const double* bias, double* y, double* s)
+{
+#pragma omp parallel for collapse(2) schedule(static)
+    for (int64_t r = 0; r < rows; ++r)
+        for (int64_t g = 0; g < G; ++g) {
+            const size_t at = ((size_t)r * (size_t)G + (size_t)g) * (size_t)D;
+            double* n = (double*)malloc(2 * (size_t)D * sizeof(double));
+            double rstd;
+            oracle_norm_row(D, eps, x + at, n, n + D, &rstd);
+            for (int64_t i = 0; i < D; ++i) {
+                const double w = weight ? weight[g * D + i] : 1.0, b = bias ? bias[g * D + i] : 0.0;
+                const double a = n[i] * w + b, sa = fabs(w) * n[D + i] + fabs(b);
+                if (z) {
+                    const double u = oracle_act(act, z[at + i]);
+                    y[at + i] = a * u;
+                    s[at + i] = sa * fabs(u);
+                } else {
+                    y[at + i] = oracle_act(act, a);
+                    s[at + i] = 1.1 * sa + fabs(y[at + i]);
+                }
+            }
+            free(n);
+        }
+}
+
+/*
+ * Its gradients for dL/dy = gy:  ga = gy act(z) and gz = gy a act'(z), or ga = gy act'(a);
+ * gbias = sum ga, gweight = sum ga n (over rows), gn = ga weight,
+ * gx = (gn - mean gn - n mean(gn n)) / sqrt(var + eps).
+ * Scales: every product with its factors' magnitudes (sn, sa above; act' of SiLU with its two
+ * terms' magnitudes; without a gate ga's scale adds |gy| sa / 2, |act''| <= 1/2), every sum of the
+ * terms' scales.
+ */
+void oracle_group_norm_gated_backward(int64_t rows, int64_t G, int64_t D, double eps, int act, const double* x,
+                                      const double* z, const double* weight, const double* bias, const double* gy,
+                                      double* gx, double* gz, double* gweight, double* gbias, double* sx, double* sz,
+                                      double* sw, double* sb)
+{
+    for (int64_t c = 0; c < G * D; ++c) gweight[c] = gbias[c] = sw[c] = sb[c] = 0.0;
+#pragma omp parallel for schedule(static)
+    for (int64_t g = 0; g < G; ++g) {
+        double* n = (double*)malloc(4 * (size_t)D * sizeof(double));
+        double *sn = n + D, *gn = n + 2 * D, *sgn = n + 3 * D;
+        for (int64_t r = 0; r < rows; ++r) {
+            const size_t at = ((size_t)r * (size_t)G + (size_t)g) * (size_t)D;
+            double rstd, m1 = 0.0, m2 = 0.0, sm1 = 0.0, sm2 = 0.0;
+            oracle_norm_row(D, eps, x + at, n, sn, &rstd);
+            for (int64_t i = 0; i < D; ++i) {
+                const int64_t c = g * D + i;
+                const double w = weight ? weight[c] : 1.0, b = bias ? bias[c] : 0.0;
+                const double a = n[i] * w + b, sa = fabs(w) * sn[i] + fabs(b);
+                const double v = z ? z[at + i] : a, p = 1.0 / (1.0 + exp(-v)), q = 1.0 / (1.0 + exp(v));
+                const double d = act == 0 ? 1.0 : act == 1 ? p + v * p * q : p * q;
+                const double ds = act == 0 ? 1.0 : act == 1 ? p + fabs(v) * p * q : p * q;
+                double ga, sga;
+                if (z) {
+                    ga = gy[at + i] * oracle_act(act, v);
+                    sga = fabs(ga);
+                    gz[at + i] = gy[at + i] * a * d;
+                    sz[at + i] = fabs(gy[at + i]) * sa * ds;
+                } else {
+                    ga = gy[at + i] * d;
+                    sga = fabs(gy[at + i]) * (ds + (act == 0 ? 0.0 : 0.5 * sa));
+                }
+                gbias[c] += ga;
+                sb[c] += sga;
+                gweight[c] += ga * n[i];
+                sw[c] += sga * sn[i];
+                gn[i] = ga * w;
+                sgn[i] = sga * fabs(w);
+                m1 += gn[i] / (double)D;
+                m2 += gn[i] * n[i] / (double)D;
+                sm1 += sgn[i] / (double)D;
+                sm2 += sgn[i] * sn[i] / (double)D;
+            }
+            for (int64_t i = 0; i < D; ++i) {
+                gx[at + i] = rstd * (gn[i] - m1 - n[i] * m2);
+                sx[at + i] = rstd * (sgn[i] + sm1 + sn[i] * sm2);
+            }
+        }
+        free(n);
+    }
+}
