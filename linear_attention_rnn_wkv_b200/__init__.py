@@ -367,44 +367,56 @@ def token_shift_mix(mu, x, x_last=None, xbar=None):
     return xbar
 
 
-def _io(t, name, like=None):
-    """Checks an fp32 or bf16 tensor; with `like`, one of its type, shape and device."""
+# The calls below are short enough on the GPU for the checks to count: one device comparison per
+# tensor (get_device, -1 on the CPU), the current stream's handle without a Stream object.
+_F32 = torch.float32
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _io(t, name):
+    """Checks an fp32 or bf16 CUDA tensor; returns its device's index."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if like is None:
-        if t.dtype not in _DTYPE:
-            raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    elif t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    elif t.shape != like.shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.get_device()
+
+
+def _like(t, name, dev, dtype, shape):
+    """Checks a tensor of the given device, type and shape."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{dev}")
     return t
 
 
-def _launch(fn, tensors, *args):
-    """Calls the library on the tensors' device and its current stream."""
-    dev = tensors[0].device
-    for t in tensors[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on one device, got {dev} and {t.device}")
-    if dev.index == torch.cuda.current_device():
-        return _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), fn.__name__)
-    with torch.cuda.device(dev):
-        return _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream), fn.__name__)
+def _launch(fn, dev, *args):
+    """Calls the library on device `dev` and its current stream."""
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, _current_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _current_stream(dev))
+    if status:
+        raise WkvError(status, fn.__name__)
 
 
-def _btc(g, x):
-    _io(g, "g")
-    if g.dim() != 3:
+def _scan_args(g, x):
+    dev = _io(g, "g")
+    shape = g.shape
+    if len(shape) != 3:
         raise ValueError("g must be [B, T, C]")
-    _io(x, "x", like=g)
-    return g.shape
-
-
-def _carry_shape(B, T, C):
-    return (B, (T + 127) // 128, C)
+    _like(x, "x", dev, g.dtype, shape)
+    return dev, shape
 
 
 def gated_scan_forward(g, x, state_in=None, want_state=True, want_carry=False, y=None, state_out=None, carry=None):
@@ -412,21 +424,21 @@ def gated_scan_forward(g, x, state_in=None, want_state=True, want_carry=False, y
     from state_in [B, C] (None: zeros): returns (y, state_out, carry).  y has g's dtype; state_out
     is [B, C] fp32 (None unless want_state or given); carry is what gated_scan_backward reads,
     [B, ceil(T / 128), C] fp32 (None unless want_carry or given)."""
-    B, T, C = _btc(g, x)
-    dev = g.device
+    dev, shape = _scan_args(g, x)
+    B, T, C = shape
     if state_in is not None:
-        _cuda_f32(state_in, "state_in", (B, C))
-    y = torch.empty_like(g) if y is None else _io(y, "y", like=g)
+        _like(state_in, "state_in", dev, _F32, (B, C))
+    y = torch.empty_like(g) if y is None else _like(y, "y", dev, g.dtype, shape)
     if state_out is not None:
-        _cuda_f32(state_out, "state_out", (B, C))
+        _like(state_out, "state_out", dev, _F32, (B, C))
     elif want_state:
-        state_out = torch.empty((B, C), dtype=torch.float32, device=dev)
+        state_out = g.new_empty((B, C), dtype=_F32)
     if carry is not None:
-        _cuda_f32(carry, "carry", _carry_shape(B, T, C))
+        _like(carry, "carry", dev, _F32, (B, (T + 127) // 128, C))
     elif want_carry:
-        carry = torch.empty(_carry_shape(B, T, C), dtype=torch.float32, device=dev)
-    _launch(lib().gated_scan_forward, (g, x, state_in, y, state_out, carry), B, T, C, _DTYPE[g.dtype], g.data_ptr(),
-            x.data_ptr(), _ptr(state_in), y.data_ptr(), _ptr(state_out), _ptr(carry))
+        carry = g.new_empty((B, (T + 127) // 128, C), dtype=_F32)
+    _launch(lib().gated_scan_forward, dev, B, T, C, _DTYPE[g.dtype], g.data_ptr(), x.data_ptr(), _ptr(state_in),
+            y.data_ptr(), _ptr(state_out), _ptr(carry))
     return y, state_out, carry
 
 
@@ -434,63 +446,62 @@ def gated_scan_backward(g, x, carry, gy, gstate_out=None, want_gstate=True, gg=N
     """Gradients of a loss of gated_scan_forward's y and state_out, given gy [B, T, C] (g's dtype)
     and gstate_out [B, C] fp32 (None: zeros), with the carry that forward wrote: returns
     (gg, gx, gstate_in); gstate_in is [B, C] fp32 (None unless want_gstate or given)."""
-    B, T, C = _btc(g, x)
-    _cuda_f32(carry, "carry", _carry_shape(B, T, C))
-    _io(gy, "gy", like=g)
+    dev, shape = _scan_args(g, x)
+    B, T, C = shape
+    _like(carry, "carry", dev, _F32, (B, (T + 127) // 128, C))
+    _like(gy, "gy", dev, g.dtype, shape)
     if gstate_out is not None:
-        _cuda_f32(gstate_out, "gstate_out", (B, C))
-    gg = torch.empty_like(g) if gg is None else _io(gg, "gg", like=g)
-    gx = torch.empty_like(g) if gx is None else _io(gx, "gx", like=g)
+        _like(gstate_out, "gstate_out", dev, _F32, (B, C))
+    gg = torch.empty_like(g) if gg is None else _like(gg, "gg", dev, g.dtype, shape)
+    gx = torch.empty_like(g) if gx is None else _like(gx, "gx", dev, g.dtype, shape)
     if gstate_in is not None:
-        _cuda_f32(gstate_in, "gstate_in", (B, C))
+        _like(gstate_in, "gstate_in", dev, _F32, (B, C))
     elif want_gstate:
-        gstate_in = torch.empty((B, C), dtype=torch.float32, device=g.device)
-    _launch(lib().gated_scan_backward, (g, x, carry, gy, gstate_out, gg, gx, gstate_in), B, T, C, _DTYPE[g.dtype],
-            g.data_ptr(), x.data_ptr(), carry.data_ptr(), gy.data_ptr(), _ptr(gstate_out), gg.data_ptr(),
-            gx.data_ptr(), _ptr(gstate_in))
+        gstate_in = g.new_empty((B, C), dtype=_F32)
+    _launch(lib().gated_scan_backward, dev, B, T, C, _DTYPE[g.dtype], g.data_ptr(), x.data_ptr(), carry.data_ptr(),
+            gy.data_ptr(), _ptr(gstate_out), gg.data_ptr(), gx.data_ptr(), _ptr(gstate_in))
     return gg, gx, gstate_in
 
 
 def gated_scan_step(g, x, state, y=None):
     """One token of the gated linear recurrence for [N, L, C] rows; state [N, L, C] fp32 is updated
     in place.  Returns y (g's dtype)."""
-    _io(g, "g")
-    if g.dim() != 3:
-        raise ValueError("g must be [N, L, C]")
-    _io(x, "x", like=g)
-    N, L, C = g.shape
-    _cuda_f32(state, "state", (N, L, C))
-    y = torch.empty_like(g) if y is None else _io(y, "y", like=g)
-    _launch(lib().gated_scan_step, (g, x, state, y), N, L, C, _DTYPE[g.dtype], g.data_ptr(), x.data_ptr(),
-            state.data_ptr(), y.data_ptr())
+    dev, shape = _scan_args(g, x)
+    N, L, C = shape
+    _like(state, "state", dev, _F32, shape)
+    y = torch.empty_like(g) if y is None else _like(y, "y", dev, g.dtype, shape)
+    _launch(lib().gated_scan_step, dev, N, L, C, _DTYPE[g.dtype], g.data_ptr(), x.data_ptr(), state.data_ptr(),
+            y.data_ptr())
     return y
 
 
 def _norm_args(x, z, weight, bias, groups, act):
-    _io(x, "x")
-    if x.dim() < 1:
+    dev = _io(x, "x")
+    shape = x.shape
+    if not shape:
         raise ValueError("x must have a channel dimension")
+    C = shape[-1]
     if z is not None:
-        _io(z, "z", like=x)
-    C = x.shape[-1]
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _cuda_f32(t, name, (C,))
+        _like(z, "z", dev, x.dtype, shape)
+    if weight is not None:
+        _like(weight, "weight", dev, _F32, (C,))
+    if bias is not None:
+        _like(bias, "bias", dev, _F32, (C,))
     if groups < 1 or C % groups:
         raise ValueError(f"groups = {groups} must divide the {C} channels")
     if act not in _ACT:
         raise ValueError(f"act must be one of {sorted(_ACT)}, got {act!r}")
-    return x.numel() // C if C else 0, C
+    return dev, x.numel() // C if C else 0, C
 
 
 def group_norm_gated(x, z=None, weight=None, bias=None, groups=1, eps=1e-5, act="silu", y=None):
     """Group norm over the last dimension of x (`groups` groups of adjacent channels per row), scaled
     by weight and shifted by bias ([C] fp32, None: 1 and 0), then gated: y = a act(z), or act(a)
     without z.  z has x's shape; act is "none", "silu" or "sigmoid".  Returns y."""
-    rows, C = _norm_args(x, z, weight, bias, groups, act)
-    y = torch.empty_like(x) if y is None else _io(y, "y", like=x)
-    _launch(lib().group_norm_gated, (x, z, weight, bias, y), rows, C, groups, _DTYPE[x.dtype], eps, _ACT[act],
-            x.data_ptr(), _ptr(z), _ptr(weight), _ptr(bias), y.data_ptr())
+    dev, rows, C = _norm_args(x, z, weight, bias, groups, act)
+    y = torch.empty_like(x) if y is None else _like(y, "y", dev, x.dtype, x.shape)
+    _launch(lib().group_norm_gated, dev, rows, C, groups, _DTYPE[x.dtype], eps, _ACT[act], x.data_ptr(), _ptr(z),
+            _ptr(weight), _ptr(bias), y.data_ptr())
     return y
 
 
@@ -499,23 +510,27 @@ def group_norm_gated_backward(x, z, weight, bias, gy, groups=1, eps=1e-5, act="s
     """Gradients of group_norm_gated given gy: returns (gx, gz, gweight, gbias); gz is None without a
     gate, gweight and gbias ([C] fp32) are None unless want_params.  A workspace passed in needs no
     initial contents and must be reused only in order."""
-    rows, C = _norm_args(x, z, weight, bias, groups, act)
-    _io(gy, "gy", like=x)
-    gx = torch.empty_like(x) if gx is None else _io(gx, "gx", like=x)
-    if z is None:
-        if gz is not None:
-            raise ValueError("gz without z")
-    else:
-        gz = torch.empty_like(x) if gz is None else _io(gz, "gz", like=x)
+    dev, rows, C = _norm_args(x, z, weight, bias, groups, act)
+    io = _DTYPE[x.dtype]
+    _like(gy, "gy", dev, x.dtype, x.shape)
+    gx = torch.empty_like(x) if gx is None else _like(gx, "gx", dev, x.dtype, x.shape)
+    if z is not None:
+        gz = torch.empty_like(x) if gz is None else _like(gz, "gz", dev, x.dtype, x.shape)
+    elif gz is not None:
+        raise ValueError("gz without z")
     gweight = gbias = ws = None
+    nbytes = 0
     if want_params:
-        both = torch.empty((2, (C + 3) // 4 * 4), dtype=torch.float32, device=x.device)
-        gweight, gbias = both[0, :C], both[1, :C]
-        nbytes = int(lib().group_norm_gated_backward_workspace_size(rows, C, groups, _DTYPE[x.dtype]))
-        ws = workspace if workspace is not None and workspace.numel() * workspace.element_size() >= nbytes else \
-            torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
-    _launch(lib().group_norm_gated_backward, (x, z, weight, bias, gy, gx, gz, gweight, ws), rows, C, groups,
-            _DTYPE[x.dtype], eps, _ACT[act], x.data_ptr(), _ptr(z), _ptr(weight), _ptr(bias), gy.data_ptr(),
-            gx.data_ptr(), _ptr(gz), _ptr(gweight), _ptr(gbias), _ptr(ws),
-            0 if ws is None else ws.numel() * ws.element_size())
+        gweight, gbias = x.new_empty((C,), dtype=_F32), x.new_empty((C,), dtype=_F32)
+        nbytes = lib().group_norm_gated_backward_workspace_size(rows, C, groups, io)
+        if workspace is None:
+            ws = x.new_empty((nbytes // 4 + 4,), dtype=_F32)
+        else:
+            ws = workspace
+            if not ws.is_cuda or ws.get_device() != dev or not ws.is_contiguous() or \
+                    ws.numel() * ws.element_size() < nbytes:
+                raise ValueError(f"workspace must be {nbytes} contiguous bytes on cuda:{dev}")
+    _launch(lib().group_norm_gated_backward, dev, rows, C, groups, io, eps, _ACT[act], x.data_ptr(), _ptr(z),
+            _ptr(weight), _ptr(bias), gy.data_ptr(), gx.data_ptr(), _ptr(gz), _ptr(gweight), _ptr(gbias), _ptr(ws),
+            nbytes)
     return gx, gz, gweight, gbias
