@@ -115,7 +115,12 @@ def _own(s):
         return wkv.gated_scan_forward(s["g"], s["x"], state_in=s["state_in"])[:2]
     if op == "scan_train":
         y, state_out, carry = wkv.gated_scan_forward(s["g"], s["x"], state_in=s["state_in"], want_carry=True)
-        return (y, state_out) + wkv.gated_scan_backward(s["g"], s["x"], carry, s["gy"], gstate_out=s["gstate"])
+        grads = wkv.gated_scan_backward(s["g"], s["x"], carry, s["gy"], gstate_out=s["gstate"])
+        if s["gy"].dtype == torch.float32:
+            # the plain form leaves the final state's gradient added to an fp32 gy; the next pass on
+            # this state has to find the same gy
+            s["gy"][:, -1] += s["gstate"]
+        return (y, state_out) + grads
     how = dict(groups=s["groups"], eps=_EPS, act=s["act"])
     y = wkv.group_norm_gated(s["x"], s["z"], s["weight"], s["bias"], **how)
     if op == "norm_fwd":
