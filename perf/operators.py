@@ -119,7 +119,7 @@ def _own(s):
         if s["gy"].dtype == torch.float32:
             # the plain form leaves the final state's gradient added to an fp32 gy; the next pass on
             # this state has to find the same gy
-            s["gy"][:, -1] += s["gstate"]
+            s["gy"].select(1, -1).add_(s["gstate"])
         return (y, state_out) + grads
     how = dict(groups=s["groups"], eps=_EPS, act=s["act"])
     y = wkv.group_norm_gated(s["x"], s["z"], s["weight"], s["bias"], **how)
