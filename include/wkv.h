@@ -351,7 +351,7 @@ wkv_status eagle_decode_step(int64_t N, int64_t L, int64_t C, const float* w, co
  * A bounded device-side wait that gives up is recorded in the device-wide word that
  * wkv_get_device_status reports (the outputs are then invalid).
  * Status codes as wkv_forward; WKV_ERR_UNSUPPORTED when B * ceil(C / 32) exceeds 2^28 - 1 (one
- * launch's blocks).
+ * launch's blocks) or C 2^23 - 1.
  */
 wkv_status gated_scan_forward(int64_t B, int64_t T, int64_t C, wkv_dtype io, const void* g, const void* x,
                               const float* state_in, void* y, float* state_out, float* carry, cudaStream_t stream);

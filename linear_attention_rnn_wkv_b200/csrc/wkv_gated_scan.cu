@@ -14,9 +14,9 @@
 //
 // Bound by HBM: g and x are read once, y written once.  B200, forward (backward) against the
 // copy rate of 6549 GB/s: 1x16384x4096 fp32 118 us, 6830 GB/s (209 us, 6410 GB/s); 4x4096x2048
-// bf16 38.4 us, 5240 GB/s (78 us, 4270 GB/s); 8x1024x768 fp32 15.0 us, 5040 GB/s (25.3 us, 4970
-// GB/s).  In bf16 a byte carries twice the tokens and the issue slots are the limit (about 22
-// instructions per token forward, 35 backward).
+// bf16 38.4 us, 5240 GB/s (73.8 us, 4550 GB/s); 8x1024x768 fp32 15.0 us, 5040 GB/s (25.3 us, 4970
+// GB/s).  In bf16 a byte carries twice the tokens and instructions are the limit (about 18 per
+// token forward, 37 backward, at half of the issue slots: two or four warps per scheduler).
 //
 // Arithmetic: fp32 whatever the I/O type.  A gate is kept as the smaller of (f, i) with a sign,
 // from e = 2^(-|g| log2 e) as e / (1 + e), relatively accurate at both ends.  A step starts from
@@ -127,9 +127,13 @@ __device__ __forceinline__ T gate_step(T s, T h, T x) { return vfma(s, vsub(h, x
 // f a: a - i a, or f a
 template <typename T>
 __device__ __forceinline__ T gate_decay(T s, T a) { return vfma(s, a, pick(s, a, zero(a))); }
-// -i a: -i a, or f a - a
+// f a, and -i a: -i a, or f a - a
 template <typename T>
-__device__ __forceinline__ T gate_input_neg(T s, T a) { return vfma(s, a, pick(s, zero(a), neg(a))); }
+__device__ __forceinline__ T gate_split(T s, T a, T& input_neg) {
+    const T kept = pick(s, a, zero(a));
+    input_neg = vfma(s, a, vsub(kept, a));  // kept - a: 0 or -a, exact
+    return vfma(s, a, kept);
+}
 // -f i = s^2 - |s|
 __device__ __forceinline__ float gate_slope_neg(float s) { return fmaf(fabsf(s), fabsf(s), -fabsf(s)); }
 __device__ __forceinline__ float2 gate_slope_neg(float2 s) { return make_float2(gate_slope_neg(s.x), gate_slope_neg(s.y)); }
@@ -245,7 +249,7 @@ struct Block {
     int lane, warp, WT, wt, W, cl;
     uint32_t S, rank;
     int64_t b, c, tile, tiles;
-    bool live, whole;  // this lane's channels exist; so do all of its warp's
+    bool live, whole;  // this lane's channels exist; so do all of the block's
 
     __device__ __forceinline__ Block(const ScanArgs& args) : a(args) {
         lane = threadIdx.x & 31;
@@ -261,7 +265,7 @@ struct Block {
         b = unit / a.groups;
         c = (unit % a.groups) * W + cl;
         live = c < a.C;
-        whole = c - lane * V + 32 * V <= a.C;
+        whole = c - cl + W <= a.C;
         tile = (int64_t)WT * LC;
         tiles = (a.T + tile - 1) / tile;
     }
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
     for (int64_t j0 = 0; j0 < tiles; j0 += S, ++it) {
         const int64_t j = j0 + rank, t0 = j * k.tile + k.wt * LC;
         if (ST && j < tiles && !ring.wait(it) && k.lane == 0) k.gave_up();
-        if (k.whole && t0 + LC <= a.T)
+        if (k.whole && (j + 1) * k.tile <= a.T)  // the same for every warp of the block
             stride(std::true_type{}, j, t0, LC);
         else
             stride(std::false_type{}, j, t0, k.live && t0 < a.T ? (int)min64(LC, a.T - t0) : 0);
@@ -424,8 +428,11 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
     using P = typename B::P;
     using Sp = Span<V>;
     extern __shared__ __align__(1024) unsigned char slots[];
-    __shared__ P wsum[2][NW][32];  // the warps' (A, H)
-    __shared__ T wadj[2][NW][32];  // and M
+    // gy stays in its slot, in 16 bits, where that is what it takes for a second block per SM
+    constexpr bool kLate = ST > 0 && sizeof(TIO) == 2;
+    constexpr int kBufs = kLate ? 1 : 2;
+    __shared__ P wsum[kBufs][NW][32];  // the warps' (A, H)
+    __shared__ T wadj[kBufs][NW][32];  // and M
     __shared__ P csum[2][kMaxCluster][32];
     __shared__ uint64_t bars[(ST ? ST : 1) + 2];
     const B k(a);
@@ -455,18 +462,31 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
     int it = 0;
     auto stride = [&](auto all, int64_t j, int64_t t0, int n) {
         constexpr bool ALL = decltype(all)::value;
-        const int64_t at = (k.b * a.T + t0) * a.C + k.c;
+        // the block's tile, and this lane's place in it: a 32-bit offset serves every array
+        const int64_t tile0 = (k.b * a.T + j * k.tile) * a.C + (k.c - k.cl);
+        const uint32_t row = (uint32_t)a.C, off = (uint32_t)(k.wt * LC) * row + (uint32_t)k.cl;
+        const TIO* gys = ST ? ring.template array<TIO>(it, 2) + k.wt * LC * k.W + k.cl : nullptr;
         T sg[LC], x[LC], gy[LC], As[LC];
+        auto gy_at = [&](int s) {
+            if constexpr (kLate) {
+                if (!ALL && s >= n) return Lanes<V>::all(0.f);
+                float t[V];
+                Vec<TIO, V>::load(gys + s * k.W, t);
+                return Lanes<V>::make(t);
+            } else {
+                return gy[s];
+            }
+        };
         // a tile is kGatedCarrySteps long, or holds the whole sequence
         T h = j >= 0 ? k.load_state(a.carry, k.b * tiles + j) : Lanes<V>::all(0.f);
         if (ST) {
             load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 0) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, sg);
             load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 1) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, x);
-            load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 2) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, gy);
+            if (!kLate) load_rows<TIO, V, LC, true>(gys, k.W, LC, 0.f, gy);
         } else {
-            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.g) + at, a.C, n, 0.f, sg);
-            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.x) + at, a.C, n, 0.f, x);
-            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.gy) + at, a.C, n, 0.f, gy);
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.g) + tile0 + off, a.C, n, 0.f, sg);
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.x) + tile0 + off, a.C, n, 0.f, x);
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.gy) + tile0 + off, a.C, n, 0.f, gy);
         }
         T A = Lanes<V>::all(1.f), H = Lanes<V>::all(0.f), M = Lanes<V>::all(0.f);
 #pragma unroll
@@ -475,7 +495,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
             if (!ALL && s >= n) {
                 sg[s] = Lanes<V>::all(-0.f);
                 x[s] = Lanes<V>::all(0.f);
-                gy[s] = Lanes<V>::all(0.f);
+                if (!kLate) gy[s] = Lanes<V>::all(0.f);
             }
             // x becomes h_{t-1} - x_t of the span from zero; the state entering adds As_t h_in to it
             As[s] = A;
@@ -485,14 +505,18 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
             x[s] = d;
         }
 #pragma unroll
-        for (int s = LC - 1; s >= 0; --s) M = gate_decay(sg[s], vsub(M, gy[s]));
-        P(*ws)[32] = wsum[it & 1];
-        T(*wm)[32] = wadj[it & 1];
+        for (int s = LC - 1; s >= 0; --s) M = gate_decay(sg[s], vsub(M, gy_at(s)));
+        P(*ws)[32] = wsum[it % kBufs];
+        T(*wm)[32] = wadj[it % kBufs];
         ws[k.warp][k.lane] = Sp::pack(A, H);
         wm[k.warp][k.lane] = M;
         if (S > 1 && threadIdx.x == 0) ex.expect(it, S);
         __syncthreads();
-        if (ST && threadIdx.x == 0 && j - (int64_t)ST * S >= 0) ring.fetch(it + ST, (j - (int64_t)ST * S) * k.tile, maps);
+        if (ST && threadIdx.x == 0) {
+            // the slot just read, or, with gy still to be read from it, the one before
+            const int ahead = kLate ? ST - 1 : ST;
+            if ((!kLate || it > 0) && j - (int64_t)ahead * S >= 0) ring.fetch(it + ahead, (j - (int64_t)ahead * S) * k.tile, maps);
+        }
         const int w0 = ST ? 0 : k.warp - k.wt, WT = ST ? NW : k.WT;
 #pragma unroll
         for (int w = 0; w < WT - 1; ++w)
@@ -528,18 +552,19 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
                 carry = vfma(Sp::A(ws[w0 + w][k.lane]), carry, wm[w0 + w][k.lane]);
             }
         }
-        TIO* gx = static_cast<TIO*>(a.y) + at;
-        TIO* gg = static_cast<TIO*>(a.gg) + at;
+        if (kBufs == 1) __syncthreads();  // read before the next tile's are written
+        TIO *gx = static_cast<TIO*>(a.y) + tile0, *gg = static_cast<TIO*>(a.gg) + tile0;
 #pragma unroll
         for (int s = LC - 1; s >= 0; --s) {
-            const T lam = vsub(m, gy[s]);  // negated, as m
+            const T lam = vsub(m, gy_at(s));  // negated, as m
             float ox[V], og[V];
-            Lanes<V>::split(gate_input_neg(sg[s], lam), ox);
+            T in;
+            m = gate_split(sg[s], lam, in);
+            Lanes<V>::split(in, ox);
             Lanes<V>::split(vmul(vmul(gate_slope_neg(sg[s]), vfma(As[s], h, x[s])), lam), og);
-            m = gate_decay(sg[s], lam);
             if (ALL || s < n) {
-                Vec<TIO, V>::store(gx + s * a.C, ox);
-                Vec<TIO, V>::store(gg + s * a.C, og);
+                Vec<TIO, V>::store(gx + off + s * row, ox);
+                Vec<TIO, V>::store(gg + off + s * row, og);
             }
         }
     };
@@ -547,7 +572,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         const int64_t j = tiles - 1 - j0 - rank;  // < 0: past the sequence's start
         const int64_t t0 = j * k.tile + k.wt * LC;
         if (ST && j >= 0 && !ring.wait(it) && k.lane == 0) k.gave_up();
-        if (k.whole && j >= 0 && t0 + LC <= a.T)
+        if (k.whole && j >= 0 && (j + 1) * k.tile <= a.T)
             stride(std::true_type{}, j, t0, LC);
         else
             stride(std::false_type{}, j, t0, k.live && j >= 0 && t0 < a.T ? (int)min64(LC, a.T - t0) : 0);
@@ -645,11 +670,11 @@ constexpr int64_t kShort = 64;
 
 bool staged_rows(const GatedScanShape& s) {
     const int64_t es = s.io == 1 ? 2 : 4;
-    return s.T > kShort && s.C * es % 16 == 0 && s.T <= INT32_MAX && s.C <= INT32_MAX &&
-           s.T * s.C * es < (int64_t(1) << 40);  // a tensor map's stride
+    return s.T > kShort && s.C * es % 16 == 0 && s.T <= INT32_MAX &&
+           s.T * s.C * es < (int64_t(1) << 40);  // a tensor map's coordinates and strides
 }
 
-// Pairs per lane halve the instructions, single channels make twice the blocks.  Pairs win where
+// fp32: pairs per lane halve the instructions, single channels make twice the blocks.  Pairs win where
 // even single channels leave the SMs to a few long sequences (1x16384x4096 fp32: forward 118
 // against 143, backward 209 against 257), single channels elsewhere (8x1024x768: 15.0 against
 // 16.3, 25.3 against 26.7).
@@ -670,14 +695,17 @@ cudaError_t launch_direct(const GatedScanShape& s, const ScanArgs& a, cudaStream
 }
 
 // The forward's staged form: 32 steps per warp and four warps (fewer summaries to fold: bf16
-// 4x4096x2048 38 against 43 with 16 steps and eight warps); bf16 always in pairs (a row of the
-// tile is then 128 bytes: 4x4096x2048 38 against 54).  The backward holds four values per token,
-// which 32 steps spill: 16 steps, eight warps.
+// 4x4096x2048 38 against 43 with 16 steps and eight warps).  The backward holds four values per
+// token, which 32 steps spill: 16 steps, eight warps.  bf16 always in pairs (a row of the tile is
+// then 128 bytes: forward 38 against 54); its backward leaves gy in the staged tile, so that two
+// blocks fit an SM (64x1024x768: 101 against 125 with gy in registers and one block).
 template <typename TIO, bool BWD>
 cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t stream) {
     constexpr bool kHalf = sizeof(TIO) == 2;
     if (staged_rows(s)) {
-        if constexpr (BWD) {
+        if constexpr (BWD && kHalf) {
+            return launch_scan<TIO, 2, 16, 8, 2, 2, true>(s, a, stream);
+        } else if constexpr (BWD) {
             if (wide_lanes(s)) return launch_scan<TIO, 2, 16, 8, 2, 1, true>(s, a, stream);
             return launch_scan<TIO, 1, 16, 8, 2, 2, true>(s, a, stream);
         } else if constexpr (kHalf) {
@@ -698,6 +726,7 @@ unsigned flat_blocks(int64_t units) {
 }  // namespace
 
 bool gated_scan_fits(const GatedScanShape& s) {
+    if (s.C > INT32_MAX / 256) return false;  // a tile's offsets are 32-bit
     // the most blocks any split takes: every 32 channels of every sequence, kMaxCluster deep
     return s.B <= INT32_MAX / kMaxCluster / ((s.C + 31) / 32);
 }

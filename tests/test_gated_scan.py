@@ -153,6 +153,7 @@ def test_validation_without_launch():
         assert call(1, 4, 4, g=FAKE + 8) == 2        # misaligned input
         assert call(1 << 28, 1, 4) == 3              # more blocks than a launch holds
         assert call(1 << 23, 1, 1024) == 3
+        assert call(1, 1, 1 << 23) == 3              # 32-bit offsets within a tile
         assert call(0, 4, 4) == 0 and call(3, 4, 0) == 0
     assert fwd(1, 4, 4, y=None) == 1
     assert fwd(1, 4, 4, y=FAKE + 4) == 2 and fwd(1, 4, 4, s=FAKE + 4) == 2
