@@ -585,23 +585,31 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
     }
 }
 
-// One token per row-channel: h <- f h + i x, y = h.  Bound by the bytes of g, x, y and the
-// state in and out.
+// One token per row-channel: h <- f h + i x, y = h, one 16-byte vector of g per thread.  Bound by the
+// bytes of g, x, y and the state in and out: 256x32x4096 fp32 98 us, 6870 GB/s (a grid of eight
+// blocks per SM walking the rows took 114).
 template <typename TIO, int V>
 __global__ void __launch_bounds__(256) step_kernel(int64_t n, const TIO* __restrict__ g, const TIO* __restrict__ x,
                                                    float* __restrict__ state, TIO* __restrict__ y) {
+    constexpr int VS = V < 4 ? V : 4;  // channels per access of the state
     grid_dep_launch_dependents();
     grid_dep_wait();  // before any global memory access
     const int64_t stride = (int64_t)gridDim.x * blockDim.x * V;
     for (int64_t k = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * V; k < n; k += stride) {
-        float gv[V], xv[V], h[V];
+        float gv[V], xv[V], h[V / VS][VS];
         Vec<TIO, V>::load(g + k, gv);
         Vec<TIO, V>::load(x + k, xv);
-        Vec<float, V>::load(state + k, h);
 #pragma unroll
-        for (int q = 0; q < V; ++q) h[q] = gate_step(gate(gv[q]), h[q], xv[q]);
-        Vec<float, V>::store(state + k, h);
-        Vec<TIO, V>::store(y + k, h);
+        for (int q = 0; q < V / VS; ++q) Vec<float, VS>::load(state + k + q * VS, h[q]);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            float& hq = h[q / VS][q % VS];
+            hq = gate_step(gate(gv[q]), hq, xv[q]);
+            gv[q] = hq;
+        }
+#pragma unroll
+        for (int q = 0; q < V / VS; ++q) Vec<float, VS>::store(state + k + q * VS, h[q]);
+        Vec<TIO, V>::store(y + k, gv);
     }
 }
 
@@ -718,9 +726,10 @@ cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream
     return s.C % 2 == 0 ? launch_direct<TIO, 2, BWD>(s, a, stream) : launch_direct<TIO, 1, BWD>(s, a, stream);
 }
 
+// blocks of 256 threads, one unit each (more units than a grid holds: the kernels loop)
 unsigned flat_blocks(int64_t units) {
-    const int64_t b = (units + 255) / 256, cap = (int64_t)sm_count() * 8;
-    return (unsigned)(b < cap ? b : cap);
+    const int64_t b = (units + 255) / 256;
+    return (unsigned)(b < INT32_MAX ? b : INT32_MAX);
 }
 
 }  // namespace
@@ -781,8 +790,8 @@ cudaError_t launch_gated_scan_step(int64_t n, int io, const void* g, const void*
     if (io == 1) {
         const __nv_bfloat16 *gg = static_cast<const __nv_bfloat16*>(g), *xx = static_cast<const __nv_bfloat16*>(x);
         __nv_bfloat16* yy = static_cast<__nv_bfloat16*>(y);
-        if (n % 4 == 0)
-            return launch_pdl(step_kernel<__nv_bfloat16, 4>, dim3(flat_blocks(n / 4)), dim3(256), 0, s, n, gg, xx, state, yy);
+        if (n % 8 == 0)
+            return launch_pdl(step_kernel<__nv_bfloat16, 8>, dim3(flat_blocks(n / 8)), dim3(256), 0, s, n, gg, xx, state, yy);
         return launch_pdl(step_kernel<__nv_bfloat16, 1>, dim3(flat_blocks(n)), dim3(256), 0, s, n, gg, xx, state, yy);
     }
     const float *gg = static_cast<const float*>(g), *xx = static_cast<const float*>(x);
