@@ -344,8 +344,8 @@ wkv_status eagle_decode_step(int64_t N, int64_t L, int64_t C, const float* w, co
  *   state_in   [B][C] fp32, or NULL for the empty state
  *   y          [B, T, C] in dtype io (written; must not overlap the inputs)
  *   state_out  [B][C] fp32, the state after the last token, or NULL (may be state_in)
- *   carry      gated_scan_carry_size() bytes (written), or NULL: [B][ceil(T / 128)][C] fp32,
- *              the state entering each 128 steps, which gated_scan_backward reads
+ *   carry      gated_scan_carry_size() bytes (written), or NULL: [B][ceil(T / 64)][C] fp32,
+ *              the state entering each 64 steps, which gated_scan_backward reads
  * T = 0 writes state_out only (state_in, or zeros).  One launch without a workspace; the sums
  * are taken in a fixed order, so equal calls give equal bits.
  * A bounded device-side wait that gives up is recorded in the device-wide word that
@@ -356,7 +356,7 @@ wkv_status eagle_decode_step(int64_t N, int64_t L, int64_t C, const float* w, co
 wkv_status gated_scan_forward(int64_t B, int64_t T, int64_t C, wkv_dtype io, const void* g, const void* x,
                               const float* state_in, void* y, float* state_out, float* carry, cudaStream_t stream);
 
-/* Bytes of the forward's `carry`: 4 per sequence, channel and 128 steps (rounded up). */
+/* Bytes of the forward's `carry`: 4 per sequence, channel and 64 steps (rounded up). */
 size_t gated_scan_carry_size(int64_t B, int64_t T, int64_t C);
 
 /*

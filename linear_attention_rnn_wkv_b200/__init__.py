@@ -423,7 +423,7 @@ def gated_scan_forward(g, x, state_in=None, want_state=True, want_carry=False, y
     """The gated linear recurrence h_t = f_t h_{t-1} + (1 - f_t) x_t, f = sigma(g), over [B, T, C]
     from state_in [B, C] (None: zeros): returns (y, state_out, carry).  y has g's dtype; state_out
     is [B, C] fp32 (None unless want_state or given); carry is what gated_scan_backward reads,
-    [B, ceil(T / 128), C] fp32 (None unless want_carry or given)."""
+    [B, ceil(T / 64), C] fp32 (None unless want_carry or given)."""
     dev, shape = _scan_args(g, x)
     B, T, C = shape
     if state_in is not None:
@@ -434,9 +434,9 @@ def gated_scan_forward(g, x, state_in=None, want_state=True, want_carry=False, y
     elif want_state:
         state_out = g.new_empty((B, C), dtype=_F32)
     if carry is not None:
-        _like(carry, "carry", dev, _F32, (B, (T + 127) // 128, C))
+        _like(carry, "carry", dev, _F32, (B, (T + 63) // 64, C))
     elif want_carry:
-        carry = g.new_empty((B, (T + 127) // 128, C), dtype=_F32)
+        carry = g.new_empty((B, (T + 63) // 64, C), dtype=_F32)
     _launch(lib().gated_scan_forward, dev, B, T, C, _DTYPE[g.dtype], g.data_ptr(), x.data_ptr(), _ptr(state_in),
             y.data_ptr(), _ptr(state_out), _ptr(carry))
     return y, state_out, carry
@@ -448,7 +448,7 @@ def gated_scan_backward(g, x, carry, gy, gstate_out=None, want_gstate=True, gg=N
     (gg, gx, gstate_in); gstate_in is [B, C] fp32 (None unless want_gstate or given)."""
     dev, shape = _scan_args(g, x)
     B, T, C = shape
-    _like(carry, "carry", dev, _F32, (B, (T + 127) // 128, C))
+    _like(carry, "carry", dev, _F32, (B, (T + 63) // 64, C))
     _like(gy, "gy", dev, g.dtype, shape)
     if gstate_out is not None:
         _like(gstate_out, "gstate_out", dev, _F32, (B, C))

@@ -8,7 +8,7 @@
 namespace wkvb {
 
 // Steps from one saved state to the next (the forward's `carry`, read by the backward).
-constexpr int kGatedCarrySteps = 128;
+constexpr int kGatedCarrySteps = 64;
 
 struct GatedScanShape {
     int64_t B, T, C;

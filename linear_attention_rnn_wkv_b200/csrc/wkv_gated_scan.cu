@@ -155,30 +155,76 @@ __device__ __forceinline__ void load_rows(const TIO* p, int64_t stride, int n, f
     }
 }
 
-// A ring of ST staged tiles (ST = 0: none, the lanes read global memory): one TMA box of ROWS
-// rows of 32 V channels per array, completion on the slot's barrier.  Thread 0 refills a slot
-// right after the block's barrier behind which every lane has its values in registers.
-template <int ARRAYS, int ST, int BOX>
+// How tiles reach the lanes: from global memory directly; staged by TMA, one box of the tile's rows
+// of 32 V channels per array (rows of a multiple of 16 bytes); or staged by 16-byte asynchronous
+// copies of each row's segment from the 16-byte boundary before it (any row), 16 bytes of pitch more
+// per row.  A copied row begins at its own shift, so a lane's V channels lie 32 apart there, not
+// side by side, and are accessed one by one.
+enum How { kDirect, kTma, kCopy };
+
+template <typename TIO, int V, int ROWS, How HOW>
+struct Tile {
+    static constexpr int kPitch = 32 * V * (int)sizeof(TIO) + (HOW == kCopy ? 16 : 0);
+    static constexpr int kBytes = ROWS * kPitch;
+};
+
+// A ring of ST staged tiles, completion on the slot's barrier.  A slot is refilled right after the
+// block's barrier behind which every lane has its values in registers: by thread 0 (TMA), or by all
+// threads (copies).
+template <typename TIO, int V, int ROWS, int THREADS, int ARRAYS, int ST, How HOW>
 struct Ring {
+    using L = Tile<TIO, V, ROWS, HOW>;
     unsigned char* slots;
     uint64_t* full;
-    int c0, b;
+    int64_t c0, b, T, C, bytes;  // first channel and sequence; lengths; bytes of an array
 
     __device__ __forceinline__ void init() {
-        for (int i = 0; i < ST; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < ST; ++i) mbar_init(&full[i], HOW == kCopy ? THREADS : 1);
     }
+    __device__ __forceinline__ bool mine() const { return HOW == kCopy || threadIdx.x == 0; }
     // the tile at step t0 into slot it % ST
-    __device__ __forceinline__ void fetch(int it, int64_t t0, const CUtensorMap* const (&maps)[ARRAYS]) {
+    __device__ __forceinline__ void fetch(int it, int64_t t0, const CUtensorMap* const (&maps)[ARRAYS],
+                                          const void* const (&from)[ARRAYS]) {
         const int slot = it % ST;
-        mbar_arrive_expect_tx(&full[slot], ARRAYS * BOX);
+        unsigned char* to = slots + (size_t)slot * ARRAYS * L::kBytes;
+        if constexpr (HOW == kTma) {
+            mbar_arrive_expect_tx(&full[slot], ARRAYS * L::kBytes);
 #pragma unroll
-        for (int k = 0; k < ARRAYS; ++k)
-            tma_load_3d(slots + (size_t)(slot * ARRAYS + k) * BOX, maps[k], c0, (int)t0, b, &full[slot]);
+            for (int k = 0; k < ARRAYS; ++k)
+                tma_load_3d(to + k * L::kBytes, maps[k], (int)c0, (int)t0, (int)b, &full[slot]);
+        } else {
+            constexpr int kChunks = L::kPitch / 16;
+            const int64_t first = ((b * T + t0) * C + c0) * (int64_t)sizeof(TIO);
+            for (int id = threadIdx.x; id < ROWS * kChunks; id += THREADS) {
+                const int r = id / kChunks, k = id % kChunks;
+                const int64_t start = first + (int64_t)r * C * (int64_t)sizeof(TIO), at = (start & ~(int64_t)15) + 16 * k;
+                // nothing past the sequence, past the segment, or past the array's last byte
+                int64_t n = t0 + r < T && at < start + 32 * V * (int64_t)sizeof(TIO) ? bytes - at : 0;
+                n = n < 0 ? 0 : n > 16 ? 16 : n;
+#pragma unroll
+                for (int q = 0; q < ARRAYS; ++q)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     smem_u32(to + q * L::kBytes + r * L::kPitch + 16 * k)),
+                                 "l"(static_cast<const unsigned char*>(from[q]) + (n > 0 ? at : 0)), "r"((uint32_t)n)
+                                 : "memory");
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[slot])) : "memory");
+        }
     }
     __device__ __forceinline__ bool wait(int it) { return mbar_wait(&full[it % ST], (it / ST) & 1, kSpinLimitDefault); }
-    template <typename TIO>
-    __device__ __forceinline__ const TIO* array(int it, int k) const {
-        return reinterpret_cast<const TIO*>(slots + (size_t)(it % ST * ARRAYS + k) * BOX);
+    // this lane's channels of row r of array k; `element`: the row's first element within the
+    // arrays, modulo 2^32
+    __device__ __forceinline__ typename Lanes<V>::T get(int it, int k, int r, uint32_t element) const {
+        const unsigned char* row = slots + (size_t)(it % ST * ARRAYS + k) * L::kBytes + r * L::kPitch;
+        float t[V];
+        if constexpr (HOW == kCopy) {
+            const TIO* p = reinterpret_cast<const TIO*>(row + (element * (uint32_t)sizeof(TIO) & 15u)) + (threadIdx.x & 31);
+#pragma unroll
+            for (int q = 0; q < V; ++q) t[q] = io<TIO>::load(p + 32 * q);
+        } else {
+            Vec<TIO, V>::load(reinterpret_cast<const TIO*>(row) + (threadIdx.x & 31) * V, t);
+        }
+        return Lanes<V>::make(t);
     }
 };
 
@@ -240,11 +286,12 @@ struct Span<2> {
 };
 
 // What both directions share: where a lane's channels and steps lie, the hand-over of the state.
-template <typename TIO, int V, int LC, int NW, int ST, int ARRAYS>
+template <int V, int LC, int NW, How HOW>
 struct Block {
     using T = typename Lanes<V>::T;
     using P = typename Span<V>::P;
-    static constexpr int kBox = LC * NW * 32 * V * (int)sizeof(TIO);
+    static constexpr bool kStaged = HOW != kDirect;
+    static constexpr int kApart = HOW == kCopy ? 32 : 1;  // from one of a lane's channels to the next
     const ScanArgs& a;
     int lane, warp, WT, wt, W, cl;
     uint32_t S, rank;
@@ -254,11 +301,11 @@ struct Block {
     __device__ __forceinline__ Block(const ScanArgs& args) : a(args) {
         lane = threadIdx.x & 31;
         warp = threadIdx.x >> 5;
-        WT = ST ? NW : 1 << a.wt_log;
-        wt = ST ? warp : warp & (WT - 1);
-        const int wc = ST ? 0 : warp >> a.wt_log;
-        W = ST ? 32 * V : (NW >> a.wt_log) * 32 * V;
-        cl = (wc * 32 + lane) * V;
+        WT = kStaged ? NW : 1 << a.wt_log;
+        wt = kStaged ? warp : warp & (WT - 1);
+        const int wc = kStaged ? 0 : warp >> a.wt_log;
+        W = kStaged ? 32 * V : (NW >> a.wt_log) * 32 * V;
+        cl = HOW == kCopy ? lane : (wc * 32 + lane) * V;
         S = cluster_size();
         rank = cluster_rank();
         const int64_t unit = blockIdx.x / S;
@@ -271,28 +318,40 @@ struct Block {
     }
     __device__ __forceinline__ T load_state(const float* p, int64_t row) const {
         float t[V];
-        if (p && live) {
-            Vec<float, V>::load(p + row * a.C + c, t);
-        } else {
 #pragma unroll
-            for (int q = 0; q < V; ++q) t[q] = 0.f;
-        }
+        for (int q = 0; q < V; ++q) t[q] = 0.f;
+        if (p && kApart == 1 && live) Vec<float, V>::load(p + row * a.C + c, t);
+        if (p && kApart != 1)
+#pragma unroll
+            for (int q = 0; q < V; ++q)
+                if (c + q * kApart < a.C) t[q] = p[row * a.C + c + q * kApart];
         return Lanes<V>::make(t);
     }
-    __device__ __forceinline__ void store_state(float* p, int64_t row, T v) const {
+    // `all`: every channel of the block exists
+    template <typename TO>
+    __device__ __forceinline__ void store(TO* p, T v, bool all) const {
         float t[V];
         Lanes<V>::split(v, t);
-        if (p && live) Vec<float, V>::store(p + row * a.C + c, t);
+        if (kApart == 1) {
+            if (all || live) Vec<TO, V>::store(p, t);
+        } else {
+#pragma unroll
+            for (int q = 0; q < V; ++q)
+                if (all || c + q * kApart < a.C) io<TO>::store(p + q * kApart, t[q]);
+        }
+    }
+    __device__ __forceinline__ void store_state(float* p, int64_t row, T v) const {
+        if (p) store(p + row * a.C + c, v, false);
     }
     __device__ __forceinline__ void gave_up() const {
         atomicCAS(a.dev_err, kDevOk, (uint32_t)kDevTimeoutCopy);
     }
 };
 
-template <typename TIO, int V, int LC, int NW, int ST, int MINB>
+template <typename TIO, int V, int LC, int NW, int ST, int MINB, How HOW>
 __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __grid_constant__ CUtensorMap mg,
                                                     const __grid_constant__ CUtensorMap mx) {
-    using B = Block<TIO, V, LC, NW, ST, 2>;
+    using B = Block<V, LC, NW, HOW>;
     using T = typename B::T;
     using P = typename B::P;
     using Sp = Span<V>;
@@ -301,9 +360,11 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
     __shared__ P csum[2][kMaxCluster][32];
     __shared__ uint64_t bars[(ST ? ST : 1) + 2];
     const B k(a);
-    Ring<2, ST ? ST : 1, B::kBox> ring{slots, bars + 2, (int)(k.c - k.cl), (int)k.b};
+    Ring<TIO, V, LC * NW, 32 * NW, 2, ST ? ST : 1, HOW> ring{slots, bars + 2, k.c - k.cl, k.b, a.T, a.C,
+                                                             a.B * a.T * a.C * (int64_t)sizeof(TIO)};
     Exchange<P> ex{csum, bars};
     const CUtensorMap* const maps[2] = {&mg, &mx};
+    const void* const from[2] = {a.g, a.x};
     const int64_t tiles = k.tiles;
     const uint32_t S = k.S, rank = k.rank;
     grid_dep_launch_dependents();
@@ -312,11 +373,15 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
         if (ST) ring.init();
         fence_mbar_init();
     }
-    __syncwarp();
+    if (HOW == kCopy)
+        __syncthreads();
+    else
+        __syncwarp();
     if (S > 1) cluster_arrive();
     grid_dep_wait();  // before any global memory access
-    if (ST && threadIdx.x == 0)
-        for (int it = 0; it < ST && (int64_t)it * S + rank < tiles; ++it) ring.fetch(it, (it * (int64_t)S + rank) * k.tile, maps);
+    if (ST && ring.mine())
+        for (int it = 0; it < ST && (int64_t)it * S + rank < tiles; ++it)
+            ring.fetch(it, (it * (int64_t)S + rank) * k.tile, maps, from);
     T carry = k.load_state(a.state_in, k.b);
     if (S > 1)
         cluster_wait();  // every block of the cluster runs and its barriers are ready
@@ -328,12 +393,17 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
         constexpr bool ALL = decltype(all)::value;
         const int64_t at = (k.b * a.T + t0) * a.C + k.c;
         T sg[LC], x[LC];
-        if (ST) {  // rows past T and channels past C came as zeros
-            load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 0) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, sg);
-            load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 1) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, x);
+        if (ST) {  // a row past T, a channel past C: zeros, or another row's values
+            const uint32_t e = (uint32_t)(at - k.cl);
+#pragma unroll
+            for (int s = 0; s < LC; ++s) {
+                sg[s] = ring.get(it, 0, k.wt * LC + s, e + s * (uint32_t)a.C);
+                x[s] = ring.get(it, 1, k.wt * LC + s, e + s * (uint32_t)a.C);
+            }
         } else {
-            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.g) + at, a.C, n, 0.f, sg);
-            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.x) + at, a.C, n, 0.f, x);
+            const int rows = k.live ? n : 0;
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.g) + at, a.C, rows, 0.f, sg);
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.x) + at, a.C, rows, 0.f, x);
         }
         T A = Lanes<V>::all(1.f), H = Lanes<V>::all(0.f);
 #pragma unroll
@@ -353,7 +423,8 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
         ws[k.warp][k.lane] = Sp::pack(A, H);
         if (S > 1 && threadIdx.x == 0) ex.expect(it, S);
         __syncthreads();
-        if (ST && threadIdx.x == 0 && j + (int64_t)ST * S < tiles) ring.fetch(it + ST, (j + (int64_t)ST * S) * k.tile, maps);
+        if (ST && ring.mine() && j + (int64_t)ST * S < tiles)
+            ring.fetch(it + ST, (j + (int64_t)ST * S) * k.tile, maps, from);
         // this warp's channels: warps w0 .. w0 + WT - 1 in time order
         const int w0 = ST ? 0 : k.warp - k.wt, WT = ST ? NW : k.WT;
         T h = carry;
@@ -385,14 +456,12 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
                 carry = vfma(Sp::A(p), carry, Sp::H(p));
             }
         }
-        if (a.carry && k.wt == 0 && j < tiles && t0 % kGatedCarrySteps == 0)
+        if (a.carry && t0 < a.T && t0 % kGatedCarrySteps == 0)
             k.store_state(a.carry, k.b * saved_states(a.T) + t0 / kGatedCarrySteps, h);
         TIO* y = static_cast<TIO*>(a.y) + at;
 #pragma unroll
         for (int s = 0; s < LC; ++s) {
-            float o[V];
-            Lanes<V>::split(vfma(sg[s], h, x[s]), o);
-            if (ALL || s < n) Vec<TIO, V>::store(y + s * a.C, o);
+            if (ALL || s < n) k.store(y + s * a.C, vfma(sg[s], h, x[s]), ALL);
         }
     };
     for (int64_t j0 = 0; j0 < tiles; j0 += S, ++it) {
@@ -401,7 +470,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
         if (k.whole && (j + 1) * k.tile <= a.T)  // the same for every warp of the block
             stride(std::true_type{}, j, t0, LC);
         else
-            stride(std::false_type{}, j, t0, k.live && t0 < a.T ? (int)min64(LC, a.T - t0) : 0);
+            stride(std::false_type{}, j, t0, t0 < a.T ? (int)min64(LC, a.T - t0) : 0);
     }
     if (rank == 0 && k.wt == 0) k.store_state(a.state_out, k.b, carry);
     if (S > 1) {  // no block leaves while another may still send to it
@@ -419,11 +488,11 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
 // forward recurrence of the tile's own steps (the warps' H, exchanged together with M): g, x and
 // gy are read once and no other per-token value is needed.  m, lam and M are kept negated: every
 // product then is one of s with no sign change on a packed operand.
-template <typename TIO, int V, int LC, int NW, int ST, int MINB>
+template <typename TIO, int V, int LC, int NW, int ST, int MINB, How HOW>
 __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __grid_constant__ CUtensorMap mg,
                                                     const __grid_constant__ CUtensorMap mx,
                                                     const __grid_constant__ CUtensorMap mgy) {
-    using B = Block<TIO, V, LC, NW, ST, 3>;
+    using B = Block<V, LC, NW, HOW>;
     using T = typename B::T;
     using P = typename B::P;
     using Sp = Span<V>;
@@ -436,9 +505,11 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
     __shared__ P csum[2][kMaxCluster][32];
     __shared__ uint64_t bars[(ST ? ST : 1) + 2];
     const B k(a);
-    Ring<3, ST ? ST : 1, B::kBox> ring{slots, bars + 2, (int)(k.c - k.cl), (int)k.b};
+    Ring<TIO, V, LC * NW, 32 * NW, 3, ST ? ST : 1, HOW> ring{slots, bars + 2, k.c - k.cl, k.b, a.T, a.C,
+                                                             a.B * a.T * a.C * (int64_t)sizeof(TIO)};
     Exchange<P> ex{csum, bars};
     const CUtensorMap* const maps[3] = {&mg, &mx, &mgy};
+    const void* const from[3] = {a.g, a.x, a.gy};
     const int64_t tiles = k.tiles;
     const uint32_t S = k.S, rank = k.rank;
     grid_dep_launch_dependents();
@@ -447,12 +518,15 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         if (ST) ring.init();
         fence_mbar_init();
     }
-    __syncwarp();
+    if (HOW == kCopy)
+        __syncthreads();
+    else
+        __syncwarp();
     if (S > 1) cluster_arrive();
     grid_dep_wait();  // before any global memory access
-    if (ST && threadIdx.x == 0)
+    if (ST && ring.mine())
         for (int it = 0; it < ST; ++it)
-            if (const int64_t j = tiles - 1 - it * (int64_t)S - rank; j >= 0) ring.fetch(it, j * k.tile, maps);
+            if (const int64_t j = tiles - 1 - it * (int64_t)S - rank; j >= 0) ring.fetch(it, j * k.tile, maps, from);
     T carry = neg(k.load_state(a.gstate, k.b));
     if (S > 1)
         cluster_wait();
@@ -465,29 +539,30 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         // the block's tile, and this lane's place in it: a 32-bit offset serves every array
         const int64_t tile0 = (k.b * a.T + j * k.tile) * a.C + (k.c - k.cl);
         const uint32_t row = (uint32_t)a.C, off = (uint32_t)(k.wt * LC) * row + (uint32_t)k.cl;
-        const TIO* gys = ST ? ring.template array<TIO>(it, 2) + k.wt * LC * k.W + k.cl : nullptr;
+        const uint32_t e = (uint32_t)tile0 + (uint32_t)(k.wt * LC) * row;  // the warp's first row begins here
         T sg[LC], x[LC], gy[LC], As[LC];
+        // a tile is a multiple of kGatedCarrySteps long, or holds the whole sequence
+        T h = j >= 0 ? k.load_state(a.carry, k.b * saved_states(a.T) + j * k.tile / kGatedCarrySteps) : Lanes<V>::all(0.f);
+        if (ST) {
+#pragma unroll
+            for (int s = 0; s < LC; ++s) {
+                sg[s] = ring.get(it, 0, k.wt * LC + s, e + s * row);
+                x[s] = ring.get(it, 1, k.wt * LC + s, e + s * row);
+                if (!kLate) gy[s] = ring.get(it, 2, k.wt * LC + s, e + s * row);
+            }
+        } else {
+            const int rows = k.live ? n : 0;
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.g) + tile0 + off, a.C, rows, 0.f, sg);
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.x) + tile0 + off, a.C, rows, 0.f, x);
+            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.gy) + tile0 + off, a.C, rows, 0.f, gy);
+        }
         auto gy_at = [&](int s) {
             if constexpr (kLate) {
-                if (!ALL && s >= n) return Lanes<V>::all(0.f);
-                float t[V];
-                Vec<TIO, V>::load(gys + s * k.W, t);
-                return Lanes<V>::make(t);
+                return !ALL && s >= n ? Lanes<V>::all(0.f) : ring.get(it, 2, k.wt * LC + s, e + s * row);
             } else {
                 return gy[s];
             }
         };
-        // a tile is kGatedCarrySteps long, or holds the whole sequence
-        T h = j >= 0 ? k.load_state(a.carry, k.b * tiles + j) : Lanes<V>::all(0.f);
-        if (ST) {
-            load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 0) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, sg);
-            load_rows<TIO, V, LC, true>(ring.template array<TIO>(it, 1) + k.wt * LC * k.W + k.cl, k.W, LC, 0.f, x);
-            if (!kLate) load_rows<TIO, V, LC, true>(gys, k.W, LC, 0.f, gy);
-        } else {
-            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.g) + tile0 + off, a.C, n, 0.f, sg);
-            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.x) + tile0 + off, a.C, n, 0.f, x);
-            load_rows<TIO, V, LC, ALL>(static_cast<const TIO*>(a.gy) + tile0 + off, a.C, n, 0.f, gy);
-        }
         T A = Lanes<V>::all(1.f), H = Lanes<V>::all(0.f), M = Lanes<V>::all(0.f);
 #pragma unroll
         for (int s = 0; s < LC; ++s) {
@@ -512,10 +587,11 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         wm[k.warp][k.lane] = M;
         if (S > 1 && threadIdx.x == 0) ex.expect(it, S);
         __syncthreads();
-        if (ST && threadIdx.x == 0) {
+        if (ST && ring.mine()) {
             // the slot just read, or, with gy still to be read from it, the one before
             const int ahead = kLate ? ST - 1 : ST;
-            if ((!kLate || it > 0) && j - (int64_t)ahead * S >= 0) ring.fetch(it + ahead, (j - (int64_t)ahead * S) * k.tile, maps);
+            if ((!kLate || it > 0) && j - (int64_t)ahead * S >= 0) 
+                ring.fetch(it + ahead, (j - (int64_t)ahead * S) * k.tile, maps, from);
         }
         const int w0 = ST ? 0 : k.warp - k.wt, WT = ST ? NW : k.WT;
 #pragma unroll
@@ -557,14 +633,12 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
 #pragma unroll
         for (int s = LC - 1; s >= 0; --s) {
             const T lam = vsub(m, gy_at(s));  // negated, as m
-            float ox[V], og[V];
             T in;
             m = gate_split(sg[s], lam, in);
-            Lanes<V>::split(in, ox);
-            Lanes<V>::split(vmul(vmul(gate_slope_neg(sg[s]), vfma(As[s], h, x[s])), lam), og);
+            const T out = vmul(vmul(gate_slope_neg(sg[s]), vfma(As[s], h, x[s])), lam);
             if (ALL || s < n) {
-                Vec<TIO, V>::store(gx + off + s * row, ox);
-                Vec<TIO, V>::store(gg + off + s * row, og);
+                k.store(gx + off + s * row, in, ALL);
+                k.store(gg + off + s * row, out, ALL);
             }
         }
     };
@@ -575,7 +649,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         if (k.whole && j >= 0 && (j + 1) * k.tile <= a.T)
             stride(std::true_type{}, j, t0, LC);
         else
-            stride(std::false_type{}, j, t0, k.live && j >= 0 && t0 < a.T ? (int)min64(LC, a.T - t0) : 0);
+            stride(std::false_type{}, j, t0, j >= 0 && t0 < a.T ? (int)min64(LC, a.T - t0) : 0);
     }
     if (rank == 0 && k.wt == 0) k.store_state(a.state_out, k.b, neg(carry));
     if (S > 1) {
@@ -628,9 +702,10 @@ int sm_count() {
 
 // One configuration: V channels per lane, LC steps per warp, NW warps per block, ST staged tiles,
 // RES blocks resident per SM.  S, the blocks of a cluster, doubles while every block is resident.
-template <typename TIO, int V, int LC, int NW, int ST, int RES, bool BWD>
+template <typename TIO, int V, int LC, int NW, int ST, int RES, bool BWD, How HOW = kTma>
 cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream) {
-    constexpr int kArrays = BWD ? 3 : 2, kSmem = ST * kArrays * LC * NW * 32 * V * (int)sizeof(TIO);
+    constexpr int kArrays = BWD ? 3 : 2, kSmem = ST * kArrays * Tile<TIO, V, LC * NW, HOW>::kBytes;
+    static_assert((ST > 0) == (HOW != kDirect), "direct loads stage nothing");
     while ((1 << a.wt_log) < NW && (ST || (int64_t)(LC << a.wt_log) < s.T)) ++a.wt_log;
     const int64_t W = (int64_t)(NW >> a.wt_log) * 32 * V, tiles = (s.T + LC * NW - 1) / (LC * NW);
     a.groups = (s.C + W - 1) / W;
@@ -639,7 +714,7 @@ cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream
     while (S < kMaxCluster && S < tiles && units * S * 2 <= room) S *= 2;
 
     CUtensorMap m[3] = {};
-    if (ST) {
+    if (HOW == kTma) {
         const void* from[3] = {a.g, a.x, a.gy};
         for (int k = 0; k < kArrays; ++k)
             if (!make_tile_map(&m[k], from[k], s.B, s.T, s.C, s.io, 32 * V, LC * NW)) return cudaErrorInvalidValue;
@@ -657,12 +732,12 @@ cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream
     cfg.attrs = at;
     cfg.numAttrs = 2;
     if constexpr (BWD) {
-        auto kern = scan_bwd<TIO, V, LC, NW, ST, RES>;
+        auto kern = scan_bwd<TIO, V, LC, NW, ST, RES, HOW>;
         if (kSmem > 0)
             if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
         return cudaLaunchKernelEx(&cfg, kern, a, m[0], m[1], m[2]);
     } else {
-        auto kern = scan_fwd<TIO, V, LC, NW, ST, RES>;
+        auto kern = scan_fwd<TIO, V, LC, NW, ST, RES, HOW>;
         if (kSmem > 0)
             if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
         return cudaLaunchKernelEx(&cfg, kern, a, m[0], m[1]);
@@ -676,9 +751,9 @@ cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream
 // and 21, 8x1024x768 15 and 26.
 constexpr int64_t kShort = 64;
 
-bool staged_rows(const GatedScanShape& s) {
+bool tma_rows(const GatedScanShape& s) {
     const int64_t es = s.io == 1 ? 2 : 4;
-    return s.T > kShort && s.C * es % 16 == 0 && s.T <= INT32_MAX &&
+    return s.C * es % 16 == 0 && s.T <= INT32_MAX &&
            s.T * s.C * es < (int64_t(1) << 40);  // a tensor map's coordinates and strides
 }
 
@@ -695,11 +770,10 @@ bool wide_lanes(const GatedScanShape& s) {
 // one saved state's steps.
 template <typename TIO, int V, bool BWD>
 cudaError_t launch_direct(const GatedScanShape& s, const ScanArgs& a, cudaStream_t stream) {
-    if (s.T == 1) return launch_scan<TIO, V, 1, 4, 0, 4, BWD>(s, a, stream);
-    if (s.T <= 4) return launch_scan<TIO, V, 4, 4, 0, 4, BWD>(s, a, stream);
-    if (s.T <= 32) return launch_scan<TIO, V, 8, 4, 0, 4, BWD>(s, a, stream);
-    if (s.T <= 64) return launch_scan<TIO, V, 8, 8, 0, 2, BWD>(s, a, stream);
-    return launch_scan<TIO, V, 16, 8, 0, 1, BWD>(s, a, stream);
+    if (s.T == 1) return launch_scan<TIO, V, 1, 4, 0, 4, BWD, kDirect>(s, a, stream);
+    if (s.T <= 4) return launch_scan<TIO, V, 4, 4, 0, 4, BWD, kDirect>(s, a, stream);
+    if (s.T <= 32) return launch_scan<TIO, V, 8, 4, 0, 4, BWD, kDirect>(s, a, stream);
+    return launch_scan<TIO, V, 8, 8, 0, 2, BWD, kDirect>(s, a, stream);
 }
 
 // The forward's staged form: 32 steps per warp and four warps (fewer summaries to fold: bf16
@@ -710,7 +784,9 @@ cudaError_t launch_direct(const GatedScanShape& s, const ScanArgs& a, cudaStream
 template <typename TIO, bool BWD>
 cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t stream) {
     constexpr bool kHalf = sizeof(TIO) == 2;
-    if (staged_rows(s)) {
+    if (s.T <= kShort)
+        return s.C % 2 == 0 ? launch_direct<TIO, 2, BWD>(s, a, stream) : launch_direct<TIO, 1, BWD>(s, a, stream);
+    if (tma_rows(s)) {
         if constexpr (BWD && kHalf) {
             return launch_scan<TIO, 2, 16, 8, 2, 2, true>(s, a, stream);
         } else if constexpr (BWD) {
@@ -723,7 +799,13 @@ cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream
             return launch_scan<TIO, 1, 32, 4, 2, 3, false>(s, a, stream);
         }
     }
-    return s.C % 2 == 0 ? launch_direct<TIO, 2, BWD>(s, a, stream) : launch_direct<TIO, 1, BWD>(s, a, stream);
+    if constexpr (BWD) {
+        if (kHalf || wide_lanes(s)) return launch_scan<TIO, 2, 16, 4, 2, kHalf ? 3 : 2, true, kCopy>(s, a, stream);
+        return launch_scan<TIO, 1, 16, 4, 2, 3, true, kCopy>(s, a, stream);
+    } else {
+        if (kHalf || wide_lanes(s)) return launch_scan<TIO, 2, 32, 4, 2, kHalf ? 2 : 1, false, kCopy>(s, a, stream);
+        return launch_scan<TIO, 1, 32, 4, 2, 2, false, kCopy>(s, a, stream);
+    }
 }
 
 // blocks of 256 threads, one unit each (more units than a grid holds: the kernels loop)

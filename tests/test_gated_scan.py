@@ -80,7 +80,7 @@ def _check_train(dtype, g, x, s0, gy, gs, use_state=True):
     _assert_close(gsi, gsr, ss, tol, 0, "gstate_in")
     for j in range(carry.shape[1]):
         ref, sc = (s0, np.abs(s0)) if j == 0 and s0 is not None else (np.zeros(so.shape), np.zeros(so.shape)) \
-            if j == 0 else (yr[:, 128 * j - 1], sr[:, 128 * j - 1])
+            if j == 0 else (yr[:, 64 * j - 1], sr[:, 64 * j - 1])
         _assert_close(carry[:, j], ref, sc, tol, 0, f"carry {j}")
     return y, so, carry, gg, gx, gsi
 
@@ -166,8 +166,8 @@ def test_validation_without_launch():
     step = lambda N, g=FAKE, st_=FAKE, y=FAKE, io=0: L.gated_scan_step(N, 2, 4, io, g, FAKE, st_, y, None)
     assert step(-1) == 1 and step(2, g=None) == 1 and step(2, st_=None) == 1 and step(2, y=FAKE + 4) == 2
     assert step(2, io=5) == 3 and step(0) == 0
-    assert L.gated_scan_carry_size(2, 128, 5) == 2 * 1 * 5 * 4
-    assert L.gated_scan_carry_size(2, 129, 5) == 2 * 2 * 5 * 4
+    assert L.gated_scan_carry_size(2, 64, 5) == 2 * 1 * 5 * 4
+    assert L.gated_scan_carry_size(2, 65, 5) == 2 * 2 * 5 * 4
     assert L.gated_scan_carry_size(2, 0, 5) == 0
 
 
@@ -369,7 +369,7 @@ def test_writes_exactly_its_outputs(shape, dtype):
     g, x, s0, gy, gs = _case(B, T, C, seed=450, dtype=dtype)
     G, X = to_gpu(g, td), to_gpu(x, td)
     bufs = {n: _padded(s, d) for n, s, d in (("y", shape, td), ("so", (B, C), torch.float32),
-                                             ("carry", (B, (T + 127) // 128, C), torch.float32), ("gg", shape, td),
+                                             ("carry", (B, (T + 63) // 64, C), torch.float32), ("gg", shape, td),
                                              ("gx", shape, td), ("gsi", (B, C), torch.float32))}
     o = {n: v for n, (_, v) in bufs.items()}
     wkv.gated_scan_forward(G, X, state_in=to_gpu(s0), y=o["y"], state_out=o["so"], carry=o["carry"])
