@@ -308,9 +308,9 @@ struct Block {
         cl = HOW == kCopy ? lane : (wc * 32 + lane) * V;
         S = cluster_size();
         rank = cluster_rank();
-        const int64_t unit = blockIdx.x / S;
-        b = unit / a.groups;
-        c = (unit % a.groups) * W + cl;
+        const uint32_t unit = blockIdx.x / S, groups = (uint32_t)a.groups;
+        b = unit / groups;
+        c = (int64_t)(unit % groups) * W + cl;
         live = c < a.C;
         whole = c - cl + W <= a.C;
         tile = (int64_t)WT * LC;
@@ -730,7 +730,7 @@ cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim = {(unsigned)S, 1, 1};
     cfg.attrs = at;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = S > 1 ? 2 : 1;
     if constexpr (BWD) {
         auto kern = scan_bwd<TIO, V, LC, NW, ST, RES, HOW>;
         if (kSmem > 0)
@@ -746,11 +746,12 @@ cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream
 
 // Times below: us on a B200 in a CUDA graph, inputs over the L2, shapes B x T x C.
 //
-// Staged tiles, for rows of a multiple of 16 bytes and sequences of more than kShort steps:
-// 64x32x2048 fp32 takes 33 staged and 13 direct (a short tile leaves warps idle), 32x128x2048 20
-// and 21, 8x1024x768 15 and 26.
+// Sequences of at most kShort steps are read directly: 64x32x2048 fp32 takes 33 staged and 13 direct
+// (a short tile leaves warps idle), 32x128x2048 20 and 21, 8x1024x768 15 and 26.
 constexpr int64_t kShort = 64;
 
+// Rows that TMA can stage: 4x1024x2048 forward 19, backward 33, in bf16 13 and 24.  Others are staged
+// by copies: 4x1024x2049 26, 42, 22 and 33 (direct loads took 25, 91, 46 and 71).
 bool tma_rows(const GatedScanShape& s) {
     const int64_t es = s.io == 1 ? 2 : 4;
     return s.C * es % 16 == 0 && s.T <= INT32_MAX &&
@@ -762,12 +763,11 @@ bool tma_rows(const GatedScanShape& s) {
 // against 143, backward 209 against 257), single channels elsewhere (8x1024x768: 15.0 against
 // 16.3, 25.3 against 26.7).
 bool wide_lanes(const GatedScanShape& s) {
-    return s.B * ((s.C + 31) / 32) < 2 * (int64_t)sm_count() && s.T >= 32 * kGatedCarrySteps;
+    return s.B * ((s.C + 31) / 32) < 2 * (int64_t)sm_count() && s.T >= 4096;
 }
 
-// Direct: the lanes read global memory.  Any row; a warp's steps no longer than the sequence
-// needs (512x1x4096 fp32 with 8 steps per warp: 38).  The backward's tile holds the sequence, or
-// one saved state's steps.
+// Direct: a block's warps hold the whole sequence, a warp no more steps than it needs (512x1x4096
+// fp32 with 8 steps per warp: 38).
 template <typename TIO, int V, bool BWD>
 cudaError_t launch_direct(const GatedScanShape& s, const ScanArgs& a, cudaStream_t stream) {
     if (s.T == 1) return launch_scan<TIO, V, 1, 4, 0, 4, BWD, kDirect>(s, a, stream);
@@ -799,13 +799,9 @@ cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream
             return launch_scan<TIO, 1, 32, 4, 2, 3, false>(s, a, stream);
         }
     }
-    if constexpr (BWD) {
-        if (kHalf || wide_lanes(s)) return launch_scan<TIO, 2, 16, 4, 2, kHalf ? 3 : 2, true, kCopy>(s, a, stream);
-        return launch_scan<TIO, 1, 16, 4, 2, 3, true, kCopy>(s, a, stream);
-    } else {
-        if (kHalf || wide_lanes(s)) return launch_scan<TIO, 2, 32, 4, 2, kHalf ? 2 : 1, false, kCopy>(s, a, stream);
-        return launch_scan<TIO, 1, 32, 4, 2, 2, false, kCopy>(s, a, stream);
-    }
+    // pairs in bf16 for the forward's 128-byte rows; the backward in tiles of 64 steps, three staged
+    if constexpr (BWD) return launch_scan<TIO, kHalf ? 2 : 1, 16, 4, 3, 2, true, kCopy>(s, a, stream);
+    return launch_scan<TIO, kHalf ? 2 : 1, 16, 8, 2, kHalf ? 1 : 2, false, kCopy>(s, a, stream);
 }
 
 // blocks of 256 threads, one unit each (more units than a grid holds: the kernels loop)
