@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "wkv_device.cuh"
@@ -700,8 +701,35 @@ int sm_count() {
     return sms;
 }
 
+// Clusters of S blocks of a kernel that are resident at once (asked once per kernel and device): they
+// lie within a GPC, so S blocks of every eight GPCs' 18 or 20 SMs do not always come out even.
+struct ClusterRoom {
+    std::atomic<int> of[64][kMaxCluster + 1] = {};
+
+    template <typename K>
+    int operator()(K kern, cudaLaunchConfig_t cfg, int S) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+        int n = of[dev][S].load(std::memory_order_relaxed);
+        if (n == 0) {
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim = {(unsigned)S, 1, 1};
+            cfg.gridDim = dim3((unsigned)S);
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+                cudaGetLastError();
+                n = 1;
+            }
+            of[dev][S].store(n, std::memory_order_relaxed);
+        }
+        return n;
+    }
+};
+
 // One configuration: V channels per lane, LC steps per warp, NW warps per block, ST staged tiles,
-// RES blocks resident per SM.  S, the blocks of a cluster, doubles while every block is resident.
+// RES blocks resident per SM.
 template <typename TIO, int V, int LC, int NW, int ST, int RES, bool BWD, How HOW = kTma>
 cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream) {
     constexpr int kArrays = BWD ? 3 : 2, kSmem = ST * kArrays * Tile<TIO, V, LC * NW, HOW>::kBytes;
@@ -709,9 +737,7 @@ cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream
     while ((1 << a.wt_log) < NW && (ST || (int64_t)(LC << a.wt_log) < s.T)) ++a.wt_log;
     const int64_t W = (int64_t)(NW >> a.wt_log) * 32 * V, tiles = (s.T + LC * NW - 1) / (LC * NW);
     a.groups = (s.C + W - 1) / W;
-    const int64_t units = s.B * a.groups, room = (int64_t)sm_count() * RES;
-    int S = 1;
-    while (S < kMaxCluster && S < tiles && units * S * 2 <= room) S *= 2;
+    const int64_t units = s.B * a.groups;
 
     CUtensorMap m[3] = {};
     if (HOW == kTma) {
@@ -720,28 +746,33 @@ cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream
             if (!make_tile_map(&m[k], from[k], s.B, s.T, s.C, s.io, 32 * V, LC * NW)) return cudaErrorInvalidValue;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * S));
     cfg.blockDim = dim3(32 * NW);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch ? 1 : 0;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim = {(unsigned)S, 1, 1};
-    cfg.attrs = at;
-    cfg.numAttrs = S > 1 ? 2 : 1;
-    if constexpr (BWD) {
-        auto kern = scan_bwd<TIO, V, LC, NW, ST, RES, HOW>;
+    auto launch = [&](auto kern, auto... maps) {
         if (kSmem > 0)
             if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
-        return cudaLaunchKernelEx(&cfg, kern, a, m[0], m[1], m[2]);
-    } else {
-        auto kern = scan_fwd<TIO, V, LC, NW, ST, RES, HOW>;
-        if (kSmem > 0)
-            if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
-        return cudaLaunchKernelEx(&cfg, kern, a, m[0], m[1]);
-    }
+        // the most blocks per cluster with every cluster resident at once, then the fewest that walk
+        // the sequence in as many strides
+        static ClusterRoom room;
+        int S = (int)min64(kMaxCluster, tiles);
+        while (S > 1 && units > room(kern, cfg, S)) --S;
+        const int64_t strides = (tiles + S - 1) / S;
+        S = (int)((tiles + strides - 1) / strides);
+        cfg.gridDim = dim3((unsigned)(units * S));
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch ? 1 : 0;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim = {(unsigned)S, 1, 1};
+        cfg.attrs = at;
+        cfg.numAttrs = S > 1 ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, kern, a, maps...);
+    };
+    if constexpr (BWD)
+        return launch(scan_bwd<TIO, V, LC, NW, ST, RES, HOW>, m[0], m[1], m[2]);
+    else
+        return launch(scan_fwd<TIO, V, LC, NW, ST, RES, HOW>, m[0], m[1]);
 }
 
 // Times below: us on a B200 in a CUDA graph, inputs over the L2, shapes B x T x C.
