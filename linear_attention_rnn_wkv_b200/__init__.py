@@ -370,7 +370,7 @@ def token_shift_mix(mu, x, x_last=None, xbar=None):
 # The calls below are short enough on the GPU for the checks to count: one device comparison per
 # tensor (get_device, -1 on the CPU), the current stream's handle without a Stream object.
 _F32 = torch.float32
-_current_stream = torch._C._cuda_getCurrentRawStream
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
 
 
 def _io(t, name):

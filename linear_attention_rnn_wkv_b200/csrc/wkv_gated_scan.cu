@@ -10,7 +10,7 @@
 // cluster adjacent tiles; a cluster walks its channels' sequence in strides of S tiles and
 // carries the state from stride to stride.  Summaries meet in (distributed) shared memory, in a
 // fixed order: no workspace, no waiting on other clusters, and the same bits on every run.
-// Tiles are staged by TMA ahead of their use where the rows allow it.
+// Tiles are staged ahead of their use, by TMA where the rows allow it.
 //
 // Bound by HBM: g and x are read once, y written once.  B200, forward (backward) against the
 // copy rate of 6549 GB/s: 1x16384x4096 fp32 118 us, 6830 GB/s (209 us, 6410 GB/s); 4x4096x2048
@@ -50,7 +50,7 @@ struct ScanArgs {
     void* y;                 // forward: y; backward: gx
     void* gg;                // backward
     float* state_out;        // forward: state_out; backward: gstate_in; [B][C] or null
-    float* carry;            // [B][tiles][C]: forward writes (or null), backward reads
+    float* carry;            // [B][saved_states(T)][C]: forward writes (or null), backward reads
     const float* gstate;     // backward: gradient of state_out, [B][C] or null
     uint32_t* dev_err;       // the library's device-wide error word
 };
@@ -309,9 +309,9 @@ struct Block {
         cl = HOW == kCopy ? lane : (wc * 32 + lane) * V;
         S = cluster_size();
         rank = cluster_rank();
-        const uint32_t unit = blockIdx.x / S, groups = (uint32_t)a.groups;
-        b = unit / groups;
-        c = (int64_t)(unit % groups) * W + cl;
+        const int64_t unit = blockIdx.x / S;
+        b = unit / a.groups;
+        c = (unit % a.groups) * W + cl;
         live = c < a.C;
         whole = c - cl + W <= a.C;
         tile = (int64_t)WT * LC;
@@ -529,6 +529,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         for (int it = 0; it < ST; ++it)
             if (const int64_t j = tiles - 1 - it * (int64_t)S - rank; j >= 0) ring.fetch(it, j * k.tile, maps, from);
     T carry = neg(k.load_state(a.gstate, k.b));
+    const int64_t states0 = k.b * saved_states(a.T);
     if (S > 1)
         cluster_wait();
     else
@@ -542,8 +543,8 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         const uint32_t row = (uint32_t)a.C, off = (uint32_t)(k.wt * LC) * row + (uint32_t)k.cl;
         const uint32_t e = (uint32_t)tile0 + (uint32_t)(k.wt * LC) * row;  // the warp's first row begins here
         T sg[LC], x[LC], gy[LC], As[LC];
-        // a tile is a multiple of kGatedCarrySteps long, or holds the whole sequence
-        T h = j >= 0 ? k.load_state(a.carry, k.b * saved_states(a.T) + j * k.tile / kGatedCarrySteps) : Lanes<V>::all(0.f);
+        // a tile is a multiple of kGatedCarrySteps long, or holds the whole sequence (j = 0)
+        T h = j >= 0 ? k.load_state(a.carry, states0 + j * (LC * NW / kGatedCarrySteps)) : Lanes<V>::all(0.f);
         if (ST) {
 #pragma unroll
             for (int s = 0; s < LC; ++s) {

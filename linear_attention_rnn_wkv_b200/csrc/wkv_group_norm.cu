@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(32 * kReduceRows) norm_reduce(int64_t C, int p
     const float* p = part + (int64_t)blockIdx.y * parts * C + c;
     float s = 0.f;
     if (c < C && out) {
-#pragma unroll 4
+#pragma unroll 8
         for (int k = slice; k < parts; k += kReduceRows) s += p[k * C];
     }
     sums[slice][lane] = s;

@@ -207,7 +207,7 @@ def test_activations_and_missing_parameters(act, gate, params):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,G,D", [(5000, 12, 64), (2500, 1, 768), (3000, 5, 65), (700, 2, 2000)])
+@pytest.mark.parametrize("rows,G,D", [(5000, 12, 64), (2500, 1, 768), (3000, 5, 65), (700, 2, 2000), (1300, 1, 4100)])
 def test_many_rows(rows, G, D, dtype):
     """More rows than one pass of the grid: the loops over rows and the sums over blocks."""
     _check(dtype, *_case(rows, G, D, 610 + D, dtype), G)
