@@ -335,9 +335,10 @@ wkv_status eagle_decode_step(int64_t N, int64_t L, int64_t C, const float* w, co
  *
  * g is the gate's logit: g = +inf keeps the state to its rounding whatever the finite x (a
  * padding token), g = -inf replaces it (h_t = x_t exactly: a document boundary).  A state buffer is
- * [rows][C] fp32, the empty state zeros.  Arithmetic is fp32 for both I/O types.  A NaN gate,
- * or a non-finite x or state, makes the later outputs of its sequence and channel non-finite
- * and touches no other channel.
+ * [rows][C] fp32, the empty state zeros.  Arithmetic is fp32 for both I/O types; x and states
+ * may reach 2^126 in magnitude (their differences are taken).  A NaN gate, or a non-finite x or
+ * state, makes the later outputs of its sequence and channel non-finite and touches no other
+ * channel.
  *
  * gated_scan_forward: prefill over [B, T, C].
  *   g, x       [B, T, C] in dtype io
@@ -420,7 +421,8 @@ wkv_status group_norm_gated(int64_t rows, int64_t C, int64_t groups, wkv_dtype i
  *   with a gate   gz = gy a act'(z),  ga = gy act(z);   without   ga = gy act'(a)
  *   gbias = sum over rows of ga,  gweight = sum over rows of ga n,  gn = ga weight
  *   gx = (gn - mean gn - n mean(gn n)) / sqrt(var + eps)   (means over the row's group)
- *   x, z, gy, gx, gz  [rows, C] in dtype io (gx, gz written; gz required with z, else NULL)
+ *   x, z, gy, gx, gz  [rows, C] in dtype io (gx, gz written, not overlapping the inputs or each
+ *                     other; gz required with z, else NULL)
  *   gweight, gbias    [C] fp32 (written), or NULL
  *   workspace         caller-owned scratch of ws_bytes >= group_norm_gated_backward_workspace_size(),
  *                     no initial contents needed, NULL when neither gweight nor gbias is wanted; one

@@ -119,6 +119,11 @@ __device__ __forceinline__ float2 pick(float2 s, float2 if_holds, float2 if_not)
 }
 __device__ __forceinline__ float neg(float a) { return -a; }
 __device__ __forceinline__ float2 neg(float2 a) { return make_float2(-a.x, -a.y); }
+// A barrier that needs a loaded value: behind it every thread of the block has its own.  A block sends
+// its first summary behind it, and the block that writes a cluster's final state has everyone's
+// summaries by then, so it may write over the state they began from.
+__device__ __forceinline__ void sync_with(float a) { __syncthreads_or(__float_as_int(a) == -1); }
+__device__ __forceinline__ void sync_with(float2 a) { __syncthreads_or((__float_as_int(a.x) & __float_as_int(a.y)) == -1); }
 __device__ __forceinline__ float zero(float) { return 0.f; }
 __device__ __forceinline__ float2 zero(float2) { return make_float2(0.f, 0.f); }
 
@@ -384,10 +389,12 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
         for (int it = 0; it < ST && (int64_t)it * S + rank < tiles; ++it)
             ring.fetch(it, (it * (int64_t)S + rank) * k.tile, maps, from);
     T carry = k.load_state(a.state_in, k.b);
-    if (S > 1)
+    if (S > 1) {
         cluster_wait();  // every block of the cluster runs and its barriers are ready
-    else
+        sync_with(carry);
+    } else {
         __syncthreads();
+    }
 
     int it = 0;
     auto stride = [&](auto all, int64_t j, int64_t t0, int n) {
@@ -530,10 +537,12 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
             if (const int64_t j = tiles - 1 - it * (int64_t)S - rank; j >= 0) ring.fetch(it, j * k.tile, maps, from);
     T carry = neg(k.load_state(a.gstate, k.b));
     const int64_t states0 = k.b * saved_states(a.T);
-    if (S > 1)
+    if (S > 1) {
         cluster_wait();
-    else
+        sync_with(carry);
+    } else {
         __syncthreads();
+    }
 
     int it = 0;
     auto stride = [&](auto all, int64_t j, int64_t t0, int n) {
@@ -710,22 +719,23 @@ struct ClusterRoom {
     template <typename K>
     int operator()(K kern, cudaLaunchConfig_t cfg, int S) {
         int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-        int n = of[dev][S].load(std::memory_order_relaxed);
-        if (n == 0) {
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+        int known = of[dev][S].load(std::memory_order_relaxed);  // the answer + 1
+        if (known == 0) {
             cudaLaunchAttribute at[1];
             at[0].id = cudaLaunchAttributeClusterDimension;
             at[0].val.clusterDim = {(unsigned)S, 1, 1};
             cfg.gridDim = dim3((unsigned)S);
             cfg.attrs = at;
             cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-                cudaGetLastError();
-                n = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+                cudaGetLastError();  // no cluster of this size
+                n = 0;
             }
-            of[dev][S].store(n, std::memory_order_relaxed);
+            of[dev][S].store(known = n + 1, std::memory_order_relaxed);
         }
-        return n;
+        return known - 1;
     }
 };
 

@@ -207,6 +207,9 @@ def test_binding_refuses_wrong_tensors():
         wkv.gated_scan_step(g, g, g.bfloat16())
     with pytest.raises(ValueError):
         wkv.gated_scan_step(g, g, g[:, :, :3])
+    off = torch.zeros(49, device="cuda")[1:].view(2, 4, 6)  # contiguous, 4 bytes past a boundary
+    with pytest.raises(wkv.WkvError):
+        wkv.gated_scan_forward(off, g)
 
 
 # ---- the kernels ----
@@ -414,3 +417,34 @@ def test_equal_calls_give_equal_bits_on_any_stream_and_in_a_graph():
     for o in outs:
         for a, b in zip(o, ref):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [4096, 4097])
+def test_offsets_beyond_32_bits(C):
+    """More than 2^31 elements: the last tokens of a long sequence, forward and backward, equal a call
+    on them alone from the state saved before them (to twice the last tokens' tolerance: two runs of
+    the same recurrence from one state)."""
+    import torch
+    wkv = _wkv()
+    T, last = 64 * 8300, 256
+    assert T * C > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(470)
+    r = lambda: torch.empty(1, T, C, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    g, x, gy = r(), r(), r()
+    y, so, carry = wkv.gated_scan_forward(g, x, want_carry=True)
+    gg, gx, _ = wkv.gated_scan_backward(g, x, carry, gy)
+    tail = [t[:, -last:].contiguous() for t in (g, x, gy)]
+    y2, so2, carry2 = wkv.gated_scan_forward(tail[0], tail[1], state_in=carry[:, (T - last) // 64].contiguous(),
+                                             want_carry=True)
+    gg2, gx2, _ = wkv.gated_scan_backward(tail[0], tail[1], carry2, tail[2])
+    tol = 2 * _tol(last, tail[0].float().cpu().numpy())
+    big = max(float(t.abs().max()) for t in (x, gy))  # bounds every state; the adjoint at most 1 / (1 - f) times gy
+    reach = big / float(torch.sigmoid(-tail[0].float()).min())
+    for a, b, scale in ((y[:, -last:], y2, big), (gx[:, -last:], gx2, big), (gg[:, -last:], gg2, 2 * big * reach)):
+        a, b = a.float(), b.float()
+        assert bool(((a - b).abs() <= 2 * tol * scale + 2 * HALF["bf16"] * b.abs()).all())
+    assert bool(((so - so2).abs() <= tol * big).all())
+    # and the first tokens, which the backward reaches last
+    head = [t[:, :last].contiguous() for t in (g, x)]
+    assert torch.equal(wkv.gated_scan_forward(*head)[0][:, :64], y[:, :64])

@@ -315,6 +315,27 @@ def test_equal_calls_give_equal_bits_on_any_stream_and_in_a_graph():
         assert all(torch.equal(p, q) for p, q in zip(o, ref))
 
 
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements: the last rows equal a call on them alone, bit for bit (a row's values do
+    not depend on the others)."""
+    import torch
+    wkv = _wkv()
+    rows, C, last = 530000, 4096, 40
+    assert rows * C > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(655)
+    r = lambda: torch.empty(rows, C, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    x, z, gy = r(), r(), r()
+    for groups in (64, 1):
+        y = wkv.group_norm_gated(x, z, groups=groups)
+        gx, gz, _, _ = wkv.group_norm_gated_backward(x, z, None, None, gy, groups=groups, want_params=False)
+        tail = [t[-last:].contiguous() for t in (x, z, gy)]
+        assert torch.equal(y[-last:], wkv.group_norm_gated(tail[0], tail[1], groups=groups))
+        gx2, gz2, _, _ = wkv.group_norm_gated_backward(tail[0], tail[1], None, None, tail[2], groups=groups,
+                                                       want_params=False)
+        assert torch.equal(gx[-last:], gx2) and torch.equal(gz[-last:], gz2)
+
+
 # ---- a layer's mixing step ----
 
 @pytest.mark.gpu
