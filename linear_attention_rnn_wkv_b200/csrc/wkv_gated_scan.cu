@@ -13,10 +13,10 @@
 // Tiles are staged ahead of their use, by TMA where the rows allow it.
 //
 // Bound by HBM: g and x are read once, y written once.  B200, forward (backward) against the
-// copy rate of 6549 GB/s: 1x16384x4096 fp32 118 us, 6830 GB/s (209 us, 6410 GB/s); 4x4096x2048
-// bf16 38.4 us, 5240 GB/s (73.8 us, 4550 GB/s); 8x1024x768 fp32 15.0 us, 5040 GB/s (25.3 us, 4970
-// GB/s).  In bf16 a byte carries twice the tokens and instructions are the limit (about 18 per
-// token forward, 37 backward, at half of the issue slots: two or four warps per scheduler).
+// copy rate of 6549 GB/s: 1x16384x4096 fp32 118 us, 6830 GB/s (210 us, 6390 GB/s); 4x4096x2048
+// bf16 38.4 us, 5240 GB/s (76.5 us, 4390 GB/s); 8x1024x768 fp32 15.0 us, 5040 GB/s (25.3 us, 4970
+// GB/s).  In bf16 a byte carries twice the tokens and instructions are the limit (18 per token
+// forward, 42 backward, at half of the issue slots: two or four warps per scheduler).
 //
 // Arithmetic: fp32 whatever the I/O type.  A gate is kept as the smaller of (f, i) with a sign,
 // from e = 2^(-|g| log2 e) as e / (1 + e), relatively accurate at both ends.  A step starts from
