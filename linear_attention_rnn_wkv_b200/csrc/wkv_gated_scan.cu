@@ -14,9 +14,9 @@
 //
 // Bound by HBM: g and x are read once, y written once.  B200, forward (backward) against the
 // copy rate of 6549 GB/s: 1x16384x4096 fp32 118 us, 6830 GB/s (210 us, 6390 GB/s); 4x4096x2048
-// bf16 38.4 us, 5240 GB/s (76.5 us, 4390 GB/s); 8x1024x768 fp32 15.0 us, 5040 GB/s (25.3 us, 4970
+// bf16 38.4 us, 5240 GB/s (76.6 us, 4380 GB/s); 8x1024x768 fp32 15.0 us, 5040 GB/s (25.3 us, 4970
 // GB/s).  In bf16 a byte carries twice the tokens and instructions are the limit (18 per token
-// forward, 42 backward, at half of the issue slots: two or four warps per scheduler).
+// forward, 42 backward, at half of the issue slots: two or three warps per scheduler).
 //
 // Arithmetic: fp32 whatever the I/O type.  A gate is kept as the smaller of (f, i) with a sign,
 // from e = 2^(-|g| log2 e) as e / (1 + e), relatively accurate at both ends.  A step starts from
@@ -821,8 +821,9 @@ cudaError_t launch_direct(const GatedScanShape& s, const ScanArgs& a, cudaStream
 // The forward's staged form: 32 steps per warp and four warps (fewer summaries to fold: bf16
 // 4x4096x2048 38 against 43 with 16 steps and eight warps).  The backward holds four values per
 // token, which 32 steps spill: 16 steps, eight warps.  bf16 always in pairs (a row of the tile is
-// then 128 bytes: forward 38 against 54); its backward leaves gy in the staged tile, so that two
-// blocks fit an SM (64x1024x768: 101 against 125 with gy in registers and one block).
+// then 128 bytes: forward 38 against 54); its backward leaves gy in the staged tile, so that more
+// blocks fit an SM: three of four warps (64x1024x768 102, 16x512x1024 20.6, 4x1024x4096 36.6), two
+// of eight (104, 22.3, 38.4), or, with gy in registers, one of eight (125, -, 49).
 template <typename TIO, bool BWD>
 cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t stream) {
     constexpr bool kHalf = sizeof(TIO) == 2;
@@ -830,7 +831,7 @@ cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream
         return s.C % 2 == 0 ? launch_direct<TIO, 2, BWD>(s, a, stream) : launch_direct<TIO, 1, BWD>(s, a, stream);
     if (tma_rows(s)) {
         if constexpr (BWD && kHalf) {
-            return launch_scan<TIO, 2, 16, 8, 2, 2, true>(s, a, stream);
+            return launch_scan<TIO, 2, 16, 4, 3, 3, true>(s, a, stream);
         } else if constexpr (BWD) {
             if (wide_lanes(s)) return launch_scan<TIO, 2, 16, 8, 2, 1, true>(s, a, stream);
             return launch_scan<TIO, 1, 16, 8, 2, 2, true>(s, a, stream);
@@ -841,7 +842,7 @@ cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream
             return launch_scan<TIO, 1, 32, 4, 2, 3, false>(s, a, stream);
         }
     }
-    // pairs in bf16 for the forward's 128-byte rows; the backward in tiles of 64 steps, three staged
+    // the backward in tiles of 64 steps, three staged
     if constexpr (BWD) return launch_scan<TIO, kHalf ? 2 : 1, 16, 4, 3, 2, true, kCopy>(s, a, stream);
     return launch_scan<TIO, kHalf ? 2 : 1, 16, 8, 2, kHalf ? 1 : 2, false, kCopy>(s, a, stream);
 }
