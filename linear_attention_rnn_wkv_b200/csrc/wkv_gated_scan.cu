@@ -740,36 +740,53 @@ struct ClusterRoom {
 };
 
 // One configuration: V channels per lane, LC steps per warp, NW warps per block, ST staged tiles,
-// RES blocks resident per SM.
+// RES blocks resident per SM; its launch for one shape.
 template <typename TIO, int V, int LC, int NW, int ST, int RES, bool BWD, How HOW = kTma>
-cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream) {
-    constexpr int kArrays = BWD ? 3 : 2, kSmem = ST * kArrays * Tile<TIO, V, LC * NW, HOW>::kBytes;
+struct ScanLaunch {
+    static constexpr int kArrays = BWD ? 3 : 2, kSmem = ST * kArrays * Tile<TIO, V, LC * NW, HOW>::kBytes;
     static_assert((ST > 0) == (HOW != kDirect), "direct loads stage nothing");
-    while ((1 << a.wt_log) < NW && (ST || (int64_t)(LC << a.wt_log) < s.T)) ++a.wt_log;
-    const int64_t W = (int64_t)(NW >> a.wt_log) * 32 * V, tiles = (s.T + LC * NW - 1) / (LC * NW);
-    a.groups = (s.C + W - 1) / W;
-    const int64_t units = s.B * a.groups;
 
-    CUtensorMap m[3] = {};
-    if (HOW == kTma) {
-        const void* from[3] = {a.g, a.x, a.gy};
-        for (int k = 0; k < kArrays; ++k)
-            if (!make_tile_map(&m[k], from[k], s.B, s.T, s.C, s.io, 32 * V, LC * NW)) return cudaErrorInvalidValue;
-    }
+    int wt_log = 0, S = 0;  // log2 of the warps along time, blocks per cluster
+    int64_t groups = 0, units = 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(32 * NW);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = stream;
-    auto launch = [&](auto kern, auto... maps) {
-        if (kSmem > 0)
-            if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
+    cudaError_t err = cudaSuccess;
+
+    static constexpr auto kernel() {
+        if constexpr (BWD)
+            return scan_bwd<TIO, V, LC, NW, ST, RES, HOW>;
+        else
+            return scan_fwd<TIO, V, LC, NW, ST, RES, HOW>;
+    }
+
+    explicit ScanLaunch(const GatedScanShape& s) {
+        while ((1 << wt_log) < NW && (ST || (int64_t)(LC << wt_log) < s.T)) ++wt_log;
+        const int64_t W = (int64_t)(NW >> wt_log) * 32 * V, tiles = (s.T + LC * NW - 1) / (LC * NW);
+        groups = (s.C + W - 1) / W;
+        units = s.B * groups;
+        cfg.blockDim = dim3(32 * NW);
+        cfg.dynamicSmemBytes = kSmem;
+        if (kSmem > 0) err = cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (err) return;
         // the most blocks per cluster with every cluster resident at once, then the fewest that walk
         // the sequence in as many strides
         static ClusterRoom room;
-        int S = (int)min64(kMaxCluster, tiles);
-        while (S > 1 && units > room(kern, cfg, S)) --S;
+        S = (int)min64(kMaxCluster, tiles);
+        while (S > 1 && units > room(kernel(), cfg, S)) --S;
         const int64_t strides = (tiles + S - 1) / S;
         S = (int)((tiles + strides - 1) / strides);
+    }
+
+    cudaError_t operator()(const GatedScanShape& s, ScanArgs a, cudaStream_t stream) {
+        if (err) return err;
+        a.wt_log = wt_log;
+        a.groups = groups;
+        CUtensorMap m[3] = {};
+        if (HOW == kTma) {
+            const void* from[3] = {a.g, a.x, a.gy};
+            for (int k = 0; k < kArrays; ++k)
+                if (!make_tile_map(&m[k], from[k], s.B, s.T, s.C, s.io, 32 * V, LC * NW)) return cudaErrorInvalidValue;
+        }
+        cfg.stream = stream;
         cfg.gridDim = dim3((unsigned)(units * S));
         cudaLaunchAttribute at[2];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -778,12 +795,16 @@ cudaError_t launch_scan(const GatedScanShape& s, ScanArgs a, cudaStream_t stream
         at[1].val.clusterDim = {(unsigned)S, 1, 1};
         cfg.attrs = at;
         cfg.numAttrs = S > 1 ? 2 : 1;
-        return cudaLaunchKernelEx(&cfg, kern, a, maps...);
-    };
-    if constexpr (BWD)
-        return launch(scan_bwd<TIO, V, LC, NW, ST, RES, HOW>, m[0], m[1], m[2]);
-    else
-        return launch(scan_fwd<TIO, V, LC, NW, ST, RES, HOW>, m[0], m[1]);
+        if constexpr (BWD)
+            return cudaLaunchKernelEx(&cfg, kernel(), a, m[0], m[1], m[2]);
+        else
+            return cudaLaunchKernelEx(&cfg, kernel(), a, m[0], m[1]);
+    }
+};
+
+template <typename TIO, int V, int LC, int NW, int ST, int RES, bool BWD, How HOW = kTma>
+cudaError_t launch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t stream) {
+    return ScanLaunch<TIO, V, LC, NW, ST, RES, BWD, HOW>(s)(s, a, stream);
 }
 
 // Times below: us on a B200 in a CUDA graph, inputs over the L2, shapes B x T x C.
@@ -800,12 +821,19 @@ bool tma_rows(const GatedScanShape& s) {
            s.T * s.C * es < (int64_t(1) << 40);  // a tensor map's coordinates and strides
 }
 
-// fp32: pairs per lane halve the instructions, single channels make twice the blocks.  Pairs win where
-// even single channels leave the SMs to a few long sequences (1x16384x4096 fp32: forward 118
-// against 143, backward 209 against 257), single channels elsewhere (8x1024x768: 15.0 against
-// 16.3, 25.3 against 26.7).
-bool wide_lanes(const GatedScanShape& s) {
-    return s.B * ((s.C + 31) / 32) < 2 * (int64_t)sm_count() && s.T >= 4096;
+// fp32: pairs per lane halve the instructions, single channels make twice the blocks.  Pairs win on
+// long sequences where their blocks fill three quarters of the SMs, one each and all at once
+// (1x16384x4096: forward 118 against 151, backward 210 against 264; 1x16384x2048: 61 against 76,
+// 111 against 125; 1x16384x1792: 61 against 66, 107 against 114), single channels elsewhere
+// (8x1024x768: 15.0 against 16.3, 25.1 against 27.3; 1x16384x1024: 38 against 45, 58 against 75;
+// 4x4096x768: 28 against 32, 52 against 57; 1x16384x5120: 187 against 198, 312 against 347).  Just on
+// either side of the rule the two are within a tenth of each other.
+constexpr int64_t kLong = 4096;
+
+template <typename PAIRS>
+bool fills_once(const PAIRS& l) {
+    const int64_t sms = sm_count(), blocks = l.units * l.S;
+    return blocks <= sms && blocks * 4 >= sms * 3;
 }
 
 // Direct: a block's warps hold the whole sequence, a warp no more steps than it needs (512x1x4096
@@ -833,12 +861,18 @@ cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream
         if constexpr (BWD && kHalf) {
             return launch_scan<TIO, 2, 16, 4, 3, 3, true>(s, a, stream);
         } else if constexpr (BWD) {
-            if (wide_lanes(s)) return launch_scan<TIO, 2, 16, 8, 2, 1, true>(s, a, stream);
+            if (s.T >= kLong) {
+                ScanLaunch<TIO, 2, 16, 8, 2, 1, true> pairs(s);
+                if (fills_once(pairs)) return pairs(s, a, stream);
+            }
             return launch_scan<TIO, 1, 16, 8, 2, 2, true>(s, a, stream);
         } else if constexpr (kHalf) {
             return launch_scan<TIO, 2, 32, 4, 2, 2, false>(s, a, stream);
         } else {
-            if (wide_lanes(s)) return launch_scan<TIO, 2, 32, 4, 2, 1, false>(s, a, stream);
+            if (s.T >= kLong) {
+                ScanLaunch<TIO, 2, 32, 4, 2, 1, false> pairs(s);
+                if (fills_once(pairs)) return pairs(s, a, stream);
+            }
             return launch_scan<TIO, 1, 32, 4, 2, 3, false>(s, a, stream);
         }
     }
