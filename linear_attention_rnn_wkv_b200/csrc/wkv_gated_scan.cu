@@ -13,10 +13,11 @@
 // Tiles are staged ahead of their use, by TMA where the rows allow it.
 //
 // Bound by HBM: g and x are read once, y written once.  B200, forward (backward) against the
-// copy rate of 6549 GB/s: 1x16384x4096 fp32 118 us, 6830 GB/s (210 us, 6390 GB/s); 4x4096x2048
-// bf16 38.4 us, 5240 GB/s (76.6 us, 4380 GB/s); 8x1024x768 fp32 15.0 us, 5040 GB/s (25.3 us, 4970
-// GB/s).  In bf16 a byte carries twice the tokens and instructions are the limit (18 per token
-// forward, 42 backward, at half of the issue slots: two or three warps per scheduler).
+// copy rate of 6549 GB/s: 1x16384x4096 fp32 118 us, 6830 GB/s (213 us, 6300 GB/s); 4x4096x2048
+// bf16 38.5 us, 5230 GB/s (74.6 us, 4500 GB/s); 64x1024x768 bf16 52.6 us, 5740 GB/s (91.4 us, 5510
+// GB/s); 8x1024x768 fp32 15.0 us, 5040 GB/s (25.3 us, 4970 GB/s).  In bf16 a byte carries twice the
+// tokens and instructions are the limit (18 per token forward, 42 backward, at half of the issue
+// slots or a little more: two or three warps per scheduler).
 //
 // Arithmetic: fp32 whatever the I/O type.  A gate is kept as the smaller of (f, i) with a sign,
 // from e = 2^(-|g| log2 e) as e / (1 + e), relatively accurate at both ends.  A step starts from
@@ -174,6 +175,12 @@ struct Tile {
     static constexpr int kBytes = ROWS * kPitch;
 };
 
+// Whether the backward stages gy in a ring of its own, with ST + 1 slots: read from there twice, it
+// takes no registers between, and the others' slots are free as soon as they are in registers.  Not
+// for copies, whose addresses would be formed twice (4x1024x2049 bf16: 46 against 31).
+template <typename TIO, How HOW>
+constexpr bool stages_gy_apart = HOW == kTma && sizeof(TIO) == 2;
+
 // A ring of ST staged tiles, completion on the slot's barrier.  A slot is refilled right after the
 // block's barrier behind which every lane has its values in registers: by thread 0 (TMA), or by all
 // threads (copies).
@@ -189,8 +196,7 @@ struct Ring {
     }
     __device__ __forceinline__ bool mine() const { return HOW == kCopy || threadIdx.x == 0; }
     // the tile at step t0 into slot it % ST
-    __device__ __forceinline__ void fetch(int it, int64_t t0, const CUtensorMap* const (&maps)[ARRAYS],
-                                          const void* const (&from)[ARRAYS]) {
+    __device__ __forceinline__ void fetch(int it, int64_t t0, const CUtensorMap* const* maps, const void* const* from) {
         const int slot = it % ST;
         unsigned char* to = slots + (size_t)slot * ARRAYS * L::kBytes;
         if constexpr (HOW == kTma) {
@@ -373,7 +379,6 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
     const void* const from[2] = {a.g, a.x};
     const int64_t tiles = k.tiles;
     const uint32_t S = k.S, rank = k.rank;
-    grid_dep_launch_dependents();
     if (threadIdx.x == 0) {
         ex.init();
         if (ST) ring.init();
@@ -473,6 +478,9 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
         }
     };
     for (int64_t j0 = 0; j0 < tiles; j0 += S, ++it) {
+        // not sooner: the next kernel's waiting blocks would crowd this one's onto fewer SMs when that
+        // kernel is this one again (bf16 backward, 4x1024x4096: 37 against 45 us)
+        if (j0 + S >= tiles) grid_dep_launch_dependents();
         const int64_t j = j0 + rank, t0 = j * k.tile + k.wt * LC;
         if (ST && j < tiles && !ring.wait(it) && k.lane == 0) k.gave_up();
         if (k.whole && (j + 1) * k.tile <= a.T)  // the same for every warp of the block
@@ -505,25 +513,27 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
     using P = typename B::P;
     using Sp = Span<V>;
     extern __shared__ __align__(1024) unsigned char slots[];
-    // gy stays in its slot, in 16 bits, where that is what it takes for a second block per SM
-    constexpr bool kLate = ST > 0 && sizeof(TIO) == 2;
-    constexpr int kBufs = kLate ? 1 : 2;
-    __shared__ P wsum[kBufs][NW][32];  // the warps' (A, H)
-    __shared__ T wadj[kBufs][NW][32];  // and M
+    // gy stays in its slot, in a ring of its own with a slot more than the other's
+    constexpr bool kLate = stages_gy_apart<TIO, HOW>;
+    constexpr int kST = ST ? ST : 1, kEarly = kLate ? 2 : 3;
+    __shared__ P wsum[2][NW][32];  // the warps' (A, H)
+    __shared__ T wadj[2][NW][32];  // and M
     __shared__ P csum[2][kMaxCluster][32];
-    __shared__ uint64_t bars[(ST ? ST : 1) + 2];
+    __shared__ uint64_t bars[2 + kST + (kLate ? kST + 1 : 0)];
     const B k(a);
-    Ring<TIO, V, LC * NW, 32 * NW, 3, ST ? ST : 1, HOW> ring{slots, bars + 2, k.c - k.cl, k.b, a.T, a.C,
-                                                             a.B * a.T * a.C * (int64_t)sizeof(TIO)};
+    const int64_t bytes = a.B * a.T * a.C * (int64_t)sizeof(TIO);
+    Ring<TIO, V, LC * NW, 32 * NW, kEarly, kST, HOW> ring{slots, bars + 2, k.c - k.cl, k.b, a.T, a.C, bytes};
+    Ring<TIO, V, LC * NW, 32 * NW, 1, kST + 1, HOW> late{slots + ST * kEarly * Tile<TIO, V, LC * NW, HOW>::kBytes,
+                                                         bars + 2 + kST, k.c - k.cl, k.b, a.T, a.C, bytes};
     Exchange<P> ex{csum, bars};
     const CUtensorMap* const maps[3] = {&mg, &mx, &mgy};
     const void* const from[3] = {a.g, a.x, a.gy};
     const int64_t tiles = k.tiles;
     const uint32_t S = k.S, rank = k.rank;
-    grid_dep_launch_dependents();
     if (threadIdx.x == 0) {
         ex.init();
         if (ST) ring.init();
+        if (kLate) late.init();
         fence_mbar_init();
     }
     if (HOW == kCopy)
@@ -532,9 +542,13 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         __syncwarp();
     if (S > 1) cluster_arrive();
     grid_dep_wait();  // before any global memory access
+    auto fetch = [&](int it, int64_t j) {
+        if (j < 0) return;
+        ring.fetch(it, j * k.tile, maps, from);
+        if (kLate) late.fetch(it, j * k.tile, maps + 2, from + 2);
+    };
     if (ST && ring.mine())
-        for (int it = 0; it < ST; ++it)
-            if (const int64_t j = tiles - 1 - it * (int64_t)S - rank; j >= 0) ring.fetch(it, j * k.tile, maps, from);
+        for (int it = 0; it < ST; ++it) fetch(it, tiles - 1 - it * (int64_t)S - rank);
     T carry = neg(k.load_state(a.gstate, k.b));
     const int64_t states0 = k.b * saved_states(a.T);
     if (S > 1) {
@@ -559,7 +573,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
             for (int s = 0; s < LC; ++s) {
                 sg[s] = ring.get(it, 0, k.wt * LC + s, e + s * row);
                 x[s] = ring.get(it, 1, k.wt * LC + s, e + s * row);
-                if (!kLate) gy[s] = ring.get(it, 2, k.wt * LC + s, e + s * row);
+                if (!kLate) gy[s] = ring.get(it, kEarly - 1, k.wt * LC + s, e + s * row);
             }
         } else {
             const int rows = k.live ? n : 0;
@@ -569,7 +583,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         }
         auto gy_at = [&](int s) {
             if constexpr (kLate) {
-                return !ALL && s >= n ? Lanes<V>::all(0.f) : ring.get(it, 2, k.wt * LC + s, e + s * row);
+                return !ALL && s >= n ? Lanes<V>::all(0.f) : late.get(it, 0, k.wt * LC + s, e + s * row);
             } else {
                 return gy[s];
             }
@@ -590,20 +604,16 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
             H = vfma(sg[s], d, pick(sg[s], H, x[s]));
             x[s] = d;
         }
+        if (kLate && j >= 0 && !late.wait(it) && k.lane == 0) k.gave_up();
 #pragma unroll
         for (int s = LC - 1; s >= 0; --s) M = gate_decay(sg[s], vsub(M, gy_at(s)));
-        P(*ws)[32] = wsum[it % kBufs];
-        T(*wm)[32] = wadj[it % kBufs];
+        P(*ws)[32] = wsum[it & 1];
+        T(*wm)[32] = wadj[it & 1];
         ws[k.warp][k.lane] = Sp::pack(A, H);
         wm[k.warp][k.lane] = M;
         if (S > 1 && threadIdx.x == 0) ex.expect(it, S);
         __syncthreads();
-        if (ST && ring.mine()) {
-            // the slot just read, or, with gy still to be read from it, the one before
-            const int ahead = kLate ? ST - 1 : ST;
-            if ((!kLate || it > 0) && j - (int64_t)ahead * S >= 0) 
-                ring.fetch(it + ahead, (j - (int64_t)ahead * S) * k.tile, maps, from);
-        }
+        if (ST && ring.mine()) fetch(it + ST, j - (int64_t)ST * S);  // gy's slot is the stride's before
         const int w0 = ST ? 0 : k.warp - k.wt, WT = ST ? NW : k.WT;
 #pragma unroll
         for (int w = 0; w < WT - 1; ++w)
@@ -639,7 +649,6 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
                 carry = vfma(Sp::A(ws[w0 + w][k.lane]), carry, wm[w0 + w][k.lane]);
             }
         }
-        if (kBufs == 1) __syncthreads();  // read before the next tile's are written
         TIO *gx = static_cast<TIO*>(a.y) + tile0, *gg = static_cast<TIO*>(a.gg) + tile0;
 #pragma unroll
         for (int s = LC - 1; s >= 0; --s) {
@@ -654,6 +663,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         }
     };
     for (int64_t j0 = 0; j0 < tiles; j0 += S, ++it) {
+        if (j0 + S >= tiles) grid_dep_launch_dependents();  // not sooner, as in the forward
         const int64_t j = tiles - 1 - j0 - rank;  // < 0: past the sequence's start
         const int64_t t0 = j * k.tile + k.wt * LC;
         if (ST && j >= 0 && !ring.wait(it) && k.lane == 0) k.gave_up();
@@ -743,7 +753,8 @@ struct ClusterRoom {
 // RES blocks resident per SM; its launch for one shape.
 template <typename TIO, int V, int LC, int NW, int ST, int RES, bool BWD, How HOW = kTma>
 struct ScanLaunch {
-    static constexpr int kArrays = BWD ? 3 : 2, kSmem = ST * kArrays * Tile<TIO, V, LC * NW, HOW>::kBytes;
+    static constexpr int kArrays = BWD ? 3 : 2;
+    static constexpr int kSmem = (ST * kArrays + (BWD && stages_gy_apart<TIO, HOW>)) * Tile<TIO, V, LC * NW, HOW>::kBytes;
     static_assert((ST > 0) == (HOW != kDirect), "direct loads stage nothing");
 
     int wt_log = 0, S = 0;  // log2 of the warps along time, blocks per cluster
@@ -813,8 +824,8 @@ cudaError_t launch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t
 // (a short tile leaves warps idle), 32x128x2048 20 and 21, 8x1024x768 15 and 26.
 constexpr int64_t kShort = 64;
 
-// Rows that TMA can stage: 4x1024x2048 forward 19, backward 33, in bf16 13 and 24.  Others are staged
-// by copies: 4x1024x2049 26, 42, 22 and 33 (direct loads took 25, 91, 46 and 71).
+// Rows that TMA can stage: 4x1024x2048 forward 19, backward 33, in bf16 13 and 26.  Others are staged
+// by copies: 4x1024x2049 26, 42, 22 and 31 (direct loads took 25, 91, 46 and 71).
 bool tma_rows(const GatedScanShape& s) {
     const int64_t es = s.io == 1 ? 2 : 4;
     return s.C * es % 16 == 0 && s.T <= INT32_MAX &&
@@ -850,8 +861,8 @@ cudaError_t launch_direct(const GatedScanShape& s, const ScanArgs& a, cudaStream
 // 4x4096x2048 38 against 43 with 16 steps and eight warps).  The backward holds four values per
 // token, which 32 steps spill: 16 steps, eight warps.  bf16 always in pairs (a row of the tile is
 // then 128 bytes: forward 38 against 54); its backward leaves gy in the staged tile, so that more
-// blocks fit an SM: three of four warps (64x1024x768 102, 16x512x1024 20.6, 4x1024x4096 36.6), two
-// of eight (104, 22.3, 38.4), or, with gy in registers, one of eight (125, -, 49).
+// blocks fit an SM: three of four warps (64x1024x768 91, 8x1024x768 17.1, 4x1024x4096 37), two of
+// four with three tiles staged (103, 22.1, 36.4), two of eight (119, 21.5, 42).
 template <typename TIO, bool BWD>
 cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t stream) {
     constexpr bool kHalf = sizeof(TIO) == 2;
@@ -859,7 +870,7 @@ cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream
         return s.C % 2 == 0 ? launch_direct<TIO, 2, BWD>(s, a, stream) : launch_direct<TIO, 1, BWD>(s, a, stream);
     if (tma_rows(s)) {
         if constexpr (BWD && kHalf) {
-            return launch_scan<TIO, 2, 16, 4, 3, 3, true>(s, a, stream);
+            return launch_scan<TIO, 2, 16, 4, 2, 3, true>(s, a, stream);
         } else if constexpr (BWD) {
             if (s.T >= kLong) {
                 ScanLaunch<TIO, 2, 16, 8, 2, 1, true> pairs(s);
