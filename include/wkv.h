@@ -436,7 +436,7 @@ wkv_status group_norm_gated_backward(int64_t rows, int64_t C, int64_t groups, wk
                                      void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* Workspace bytes group_norm_gated_backward needs for gweight and gbias: 8 per channel and block
- * of rows (at most 1184 blocks); 0 for an invalid or empty shape.  No device call. */
+ * of rows (at most 1480 blocks); 0 for an invalid or empty shape.  No device call. */
 size_t group_norm_gated_backward_workspace_size(int64_t rows, int64_t C, int64_t groups, wkv_dtype io);
 
 /* Human-readable name of a status code (static string). */

@@ -143,6 +143,21 @@ def test_validation_without_launch():
     assert L.group_norm_gated_backward_workspace_size(1 << 20, 4096, 64, 1) <= 8 * 4096 * 1184
 
 
+def test_workspace_size_bound():
+    """8 bytes per channel and block of rows, at most 1480 blocks (ten of 128 threads on each SM)."""
+    size = _wkv().lib().group_norm_gated_backward_workspace_size
+    most = 0
+    for io in (0, 1):
+        for D in (1, 3, 4, 8, 64, 65, 130, 520, 1030, 2048, 4096, 20000):
+            for G in (1, 5, 64):
+                for rows in (1, 7, 1000, 10 ** 7):
+                    blocks, rest = divmod(size(rows, G * D, G, io), 8 * G * D)
+                    assert rest == 0 and 1 <= blocks <= min(rows, 1480)
+                    most = max(most, blocks)
+    assert most == 1480
+    assert size(0, 64, 1, 0) == size(8, 0, 1, 0) == size(8, 64, 3, 0) == size(8, 64, 0, 0) == 0
+
+
 def test_binding_refuses_cpu_tensors():
     import torch
     wkv = _wkv()
