@@ -727,9 +727,8 @@ struct ClusterRoom {
     std::atomic<int> of[64][kMaxCluster + 1] = {};
 
     template <typename K>
-    int operator()(K kern, cudaLaunchConfig_t cfg, int S) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int operator()(int dev, K kern, cudaLaunchConfig_t cfg, int S) {
+        if (dev < 0 || dev >= 64) return 0;
         int known = of[dev][S].load(std::memory_order_relaxed);  // the answer + 1
         if (known == 0) {
             cudaLaunchAttribute at[1];
@@ -739,7 +738,8 @@ struct ClusterRoom {
             cfg.attrs = at;
             cfg.numAttrs = 1;
             int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) != cudaSuccess ||
+                cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
                 cudaGetLastError();  // no cluster of this size
                 n = 0;
             }
@@ -758,9 +758,9 @@ struct ScanLaunch {
     static_assert((ST > 0) == (HOW != kDirect), "direct loads stage nothing");
 
     int wt_log = 0, S = 0;  // log2 of the warps along time, blocks per cluster
-    int64_t groups = 0, units = 0;
+    int64_t groups = 0, units = 0, strides = 0;
+    bool capped = false;  // a cluster could not have more blocks, where there was room for them
     cudaLaunchConfig_t cfg = {};
-    cudaError_t err = cudaSuccess;
 
     static constexpr auto kernel() {
         if constexpr (BWD)
@@ -776,19 +776,21 @@ struct ScanLaunch {
         units = s.B * groups;
         cfg.blockDim = dim3(32 * NW);
         cfg.dynamicSmemBytes = kSmem;
-        if (kSmem > 0) err = cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (err) return;
+        int dev = -1;
+        cudaGetDevice(&dev);
         // the most blocks per cluster with every cluster resident at once, then the fewest that walk
         // the sequence in as many strides
         static ClusterRoom room;
         S = (int)min64(kMaxCluster, tiles);
-        while (S > 1 && units > room(kernel(), cfg, S)) --S;
-        const int64_t strides = (tiles + S - 1) / S;
+        while (S > 1 && units > room(dev, kernel(), cfg, S)) --S;
+        capped = S == kMaxCluster && tiles > kMaxCluster;
+        strides = (tiles + S - 1) / S;
         S = (int)((tiles + strides - 1) / strides);
     }
 
     cudaError_t operator()(const GatedScanShape& s, ScanArgs a, cudaStream_t stream) {
-        if (err) return err;
+        if (kSmem > 0)
+            if (cudaError_t e = cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) return e;
         a.wt_log = wt_log;
         a.groups = groups;
         CUtensorMap m[3] = {};
@@ -825,7 +827,7 @@ cudaError_t launch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t
 constexpr int64_t kShort = 64;
 
 // Rows that TMA can stage: 4x1024x2048 forward 19, backward 33, in bf16 13 and 26.  Others are staged
-// by copies: 4x1024x2049 26, 42, 22 and 31 (direct loads took 25, 91, 46 and 71).
+// by copies: 4x1024x2049 25, 42, 20 and 31 (direct loads took 25, 91, 46 and 71).
 bool tma_rows(const GatedScanShape& s) {
     const int64_t es = s.io == 1 ? 2 : 4;
     return s.C * es % 16 == 0 && s.T <= INT32_MAX &&
@@ -833,18 +835,31 @@ bool tma_rows(const GatedScanShape& s) {
 }
 
 // fp32: pairs per lane halve the instructions, single channels make twice the blocks.  Pairs win on
-// long sequences where their blocks fill three quarters of the SMs, one each and all at once
-// (1x16384x4096: forward 118 against 151, backward 210 against 264; 1x16384x2048: 61 against 76,
-// 111 against 125; 1x16384x1792: 61 against 66, 107 against 114), single channels elsewhere
-// (8x1024x768: 15.0 against 16.3, 25.1 against 27.3; 1x16384x1024: 38 against 45, 58 against 75;
-// 4x4096x768: 28 against 32, 52 against 57; 1x16384x5120: 187 against 198, 312 against 347).  Just on
-// either side of the rule the two are within a tenth of each other.
+// long sequences where their blocks, in clusters of at most four, fill three quarters of the SMs, one
+// each and all at once (1x16384x4096: forward 118 against 151, backward 210 against 264;
+// 1x16384x2048: 61 against 76, 111 against 125; 1x16384x1792: 61 against 66, 107 against 114), single
+// channels elsewhere (8x1024x768: 15.0 against 16.3, 25.1 against 27.3; 4x4096x768: 28 against 32, 52
+// against 57; 1x16384x5120: 187 against 198, 312 against 347; in clusters of five, 2x4096x768: 15
+// against 18, 27 against 29).  Just on either side of the rule the two are within a tenth of each other.
+//
+// Few channels: a cluster ends at eight blocks and the SMs are not filled, so what counts is how many
+// strides the sequence takes.  A tile of 256 steps takes the fewest while there is an SM for each of
+// its blocks: forward fp32 (bf16), 1x16384x64 16 against 21 (15 against 28), x768 28 against 32 (25
+// against 34), x1024 33 against 35 (29 against 38); backward 28 against 32 (28 against 59), 50
+// against 52 (46 against 70).  The bf16 backward, whose tile otherwise is 64 steps, has one of 128 in
+// between: pairs, or single channels where those take fewer strides (1x16384x1536 pairs 75, single
+// channels 85, the tile of 64 80; 1x4096x768 14.6, 15.2, 19; 2x1000x512 9.2, 6.6, 8.2).  Rows staged by
+// copies likewise: forward 1x16384x257 32 against 39 (30 against 47), x769 51 against 56 (48, 48);
+// backward tile 128 50 against 71, 83 against 91, 256 (43 against 94, 69 against 95).
 constexpr int64_t kLong = 4096;
 
-template <typename PAIRS>
-bool fills_once(const PAIRS& l) {
-    const int64_t sms = sm_count(), blocks = l.units * l.S;
-    return blocks <= sms && blocks * 4 >= sms * 3;
+template <typename LAUNCH>
+bool one_per_sm(const LAUNCH& l) {
+    return l.units * l.S <= sm_count();
+}
+template <typename LAUNCH>
+bool fills_once(const LAUNCH& l) {
+    return one_per_sm(l) && l.S <= 4 && l.units * l.S * 4 >= (int64_t)sm_count() * 3;
 }
 
 // Direct: a block's warps hold the whole sequence, a warp no more steps than it needs (512x1x4096
@@ -869,27 +884,55 @@ cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream
     if (s.T <= kShort)
         return s.C % 2 == 0 ? launch_direct<TIO, 2, BWD>(s, a, stream) : launch_direct<TIO, 1, BWD>(s, a, stream);
     if (tma_rows(s)) {
-        if constexpr (BWD && kHalf) {
-            return launch_scan<TIO, 2, 16, 4, 2, 3, true>(s, a, stream);
-        } else if constexpr (BWD) {
+        if constexpr (!kHalf)
             if (s.T >= kLong) {
-                ScanLaunch<TIO, 2, 16, 8, 2, 1, true> pairs(s);
+                ScanLaunch<TIO, 2, BWD ? 16 : 32, BWD ? 8 : 4, 2, 1, BWD> pairs(s);
                 if (fills_once(pairs)) return pairs(s, a, stream);
             }
-            return launch_scan<TIO, 1, 16, 8, 2, 2, true>(s, a, stream);
-        } else if constexpr (kHalf) {
-            return launch_scan<TIO, 2, 32, 4, 2, 2, false>(s, a, stream);
+        if constexpr (!BWD) {
+            ScanLaunch<TIO, kHalf ? 2 : 1, 32, 4, 2, kHalf ? 2 : 3, false> base(s);
+            if (base.strides > 1) {
+                ScanLaunch<TIO, 1, 32, 8, 2, 1, false> tall(s);
+                if (one_per_sm(tall) && tall.strides <= base.strides) return tall(s, a, stream);
+            }
+            return base(s, a, stream);
         } else {
-            if (s.T >= kLong) {
-                ScanLaunch<TIO, 2, 32, 4, 2, 1, false> pairs(s);
-                if (fills_once(pairs)) return pairs(s, a, stream);
+            ScanLaunch<TIO, 1, 16, 8, 2, 2, true> mid(s);
+            if constexpr (kHalf) {
+                ScanLaunch<TIO, 2, 16, 4, 2, 3, true> base(s);
+                if (!base.capped) return base(s, a, stream);
             }
-            return launch_scan<TIO, 1, 32, 4, 2, 3, false>(s, a, stream);
+            if (mid.strides > 1) {
+                ScanLaunch<TIO, 1, 16, 16, 2, 1, true> tall(s);
+                if (one_per_sm(tall) && tall.strides < mid.strides) return tall(s, a, stream);
+            }
+            if constexpr (kHalf) {
+                ScanLaunch<TIO, 2, 16, 8, 2, 2, true> pairs(s);
+                if (pairs.strides <= mid.strides) return pairs(s, a, stream);
+            }
+            return mid(s, a, stream);
         }
     }
-    // the backward in tiles of 64 steps, three staged
-    if constexpr (BWD) return launch_scan<TIO, kHalf ? 2 : 1, 16, 4, 3, 2, true, kCopy>(s, a, stream);
-    return launch_scan<TIO, kHalf ? 2 : 1, 16, 8, 2, kHalf ? 1 : 2, false, kCopy>(s, a, stream);
+    // by copies: as above, the backward in tiles of 64 steps, three staged
+    if constexpr (!BWD) {
+        ScanLaunch<TIO, kHalf ? 2 : 1, 16, 8, 2, 2, false, kCopy> base(s);
+        if (base.strides > 1) {
+            ScanLaunch<TIO, 1, 16, 16, 2, 1, false, kCopy> tall(s);
+            if (one_per_sm(tall) && tall.strides < base.strides) return tall(s, a, stream);
+        }
+        return base(s, a, stream);
+    } else {
+        ScanLaunch<TIO, kHalf ? 2 : 1, 16, 4, 3, 2, true, kCopy> base(s);
+        if (base.capped) {
+            ScanLaunch<TIO, 1, 16, 8, 2, kHalf ? 2 : 1, true, kCopy> mid(s);
+            if constexpr (kHalf) {  // in fp32 a tile of 256 steps does not fit
+                ScanLaunch<TIO, 1, 16, 16, 2, 1, true, kCopy> tall(s);
+                if (one_per_sm(tall) && tall.strides < mid.strides) return tall(s, a, stream);
+            }
+            if (mid.strides < base.strides) return mid(s, a, stream);
+        }
+        return base(s, a, stream);
+    }
 }
 
 // blocks of 256 threads, one unit each (more units than a grid holds: the kernels loop)
