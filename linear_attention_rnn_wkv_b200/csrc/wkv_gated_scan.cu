@@ -10,7 +10,8 @@
 // cluster adjacent tiles; a cluster walks its channels' sequence in strides of S tiles and
 // carries the state from stride to stride.  Summaries meet in (distributed) shared memory, in a
 // fixed order: no workspace, no waiting on other clusters, and the same bits on every run.
-// Tiles are staged ahead of their use, by TMA where the rows allow it.
+// Tiles are staged ahead of their use, by TMA where the rows allow it.  Where short sequences have
+// channels enough for every warp, nothing is split: a warp walks its channels' whole sequence.
 //
 // Bound by HBM: g and x are read once, y written once.  B200, forward (backward) against the
 // copy rate of 6549 GB/s: 1x16384x4096 fp32 118 us, 6830 GB/s (213 us, 6300 GB/s); 4x4096x2048
@@ -680,6 +681,123 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
     }
 }
 
+// Many channels: a warp walks the whole sequence of 32 V channels, U rows at a time, with nothing to
+// exchange.  `groups` counts groups of 32 V channels.
+template <int V>
+struct Rows {
+    using T = typename Lanes<V>::T;
+    const ScanArgs& a;
+    int64_t b, c;
+    bool live;
+
+    __device__ __forceinline__ Rows(const ScanArgs& args) : a(args) {
+        const int64_t unit = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+        b = unit / a.groups;
+        c = (unit % a.groups) * (32 * V) + (threadIdx.x & 31) * V;
+        live = b < a.B && c < a.C;
+    }
+    __device__ __forceinline__ T load(const float* p, int64_t row) const {
+        float t[V];
+#pragma unroll
+        for (int q = 0; q < V; ++q) t[q] = 0.f;
+        if (p) Vec<float, V>::load(p + row * a.C + c, t);
+        return Lanes<V>::make(t);
+    }
+    template <typename TO>
+    __device__ __forceinline__ void store(TO* p, T v) const {
+        float t[V];
+        Lanes<V>::split(v, t);
+        Vec<TO, V>::store(p, t);
+    }
+};
+
+template <typename TIO, int V, int U>
+__global__ void __launch_bounds__(128) rows_fwd(ScanArgs a) {
+    using T = typename Lanes<V>::T;
+    const Rows<V> k(a);
+    grid_dep_wait();  // before any global memory access
+    if (k.live) {
+        const int64_t at = k.b * a.T * a.C + k.c;
+        T h = k.load(a.state_in, k.b);
+        auto rows = [&](auto all, int64_t t0, int n) {
+            constexpr bool ALL = decltype(all)::value;
+            T s[U], x[U];
+            load_rows<TIO, V, U, ALL>(static_cast<const TIO*>(a.g) + at + t0 * a.C, a.C, n, 0.f, s);
+            load_rows<TIO, V, U, ALL>(static_cast<const TIO*>(a.x) + at + t0 * a.C, a.C, n, 0.f, x);
+            if (a.carry && t0 % kGatedCarrySteps == 0)
+                k.store(a.carry + (k.b * saved_states(a.T) + t0 / kGatedCarrySteps) * a.C + k.c, h);
+            TIO* y = static_cast<TIO*>(a.y) + at + t0 * a.C;
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (ALL || i < n) {
+                    h = gate_step(gate(s[i]), h, x[i]);
+                    k.store(y + i * a.C, h);
+                }
+        };
+        int64_t t0 = 0;
+        for (; t0 + U <= a.T; t0 += U) rows(std::true_type{}, t0, U);
+        if (t0 < a.T) rows(std::false_type{}, t0, (int)(a.T - t0));
+        if (a.state_out) k.store(a.state_out + k.b * a.C + k.c, h);
+    }
+    grid_dep_launch_dependents();
+}
+
+// At most kGatedCarrySteps steps, walked forward for s and h_{t-1} - x_t, which wait in shared memory (a
+// lane reads only what it wrote), and then backward.
+template <typename TIO, int V, int U>
+__global__ void __launch_bounds__(128) rows_bwd(ScanArgs a) {
+    using T = typename Lanes<V>::T;
+    using P = typename Span<V>::P;
+    using Sp = Span<V>;
+    extern __shared__ __align__(16) unsigned char slots[];
+    const Rows<V> k(a);
+    grid_dep_wait();  // before any global memory access
+    if (k.live) {
+        const int steps = (int)a.T;
+        P* const kept = reinterpret_cast<P*>(slots) + (threadIdx.x >> 5) * steps * 32 + (threadIdx.x & 31);
+        const int64_t at = k.b * a.T * a.C + k.c;
+        T m = neg(k.load(a.gstate, k.b)), h = k.load(a.carry, k.b);
+        auto forward = [&](auto all, int t0, int n) {
+            constexpr bool ALL = decltype(all)::value;
+            T s[U], x[U];
+            load_rows<TIO, V, U, ALL>(static_cast<const TIO*>(a.g) + at + (int64_t)t0 * a.C, a.C, n, 0.f, s);
+            load_rows<TIO, V, U, ALL>(static_cast<const TIO*>(a.x) + at + (int64_t)t0 * a.C, a.C, n, 0.f, x);
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (ALL || i < n) {
+                    const T sg = gate(s[i]), d = vsub(h, x[i]);
+                    kept[(t0 + i) * 32] = Sp::pack(sg, d);
+                    h = vfma(sg, d, pick(sg, h, x[i]));
+                }
+        };
+        auto backward = [&](auto all, int t0, int n) {
+            constexpr bool ALL = decltype(all)::value;
+            T gy[U];
+            load_rows<TIO, V, U, ALL>(static_cast<const TIO*>(a.gy) + at + (int64_t)t0 * a.C, a.C, n, 0.f, gy);
+            TIO *gx = static_cast<TIO*>(a.y) + at + (int64_t)t0 * a.C, *gg = static_cast<TIO*>(a.gg) + at + (int64_t)t0 * a.C;
+#pragma unroll
+            for (int i = U - 1; i >= 0; --i)
+                if (ALL || i < n) {
+                    const P p = kept[(t0 + i) * 32];
+                    const T sg = Sp::A(p), lam = vsub(m, gy[i]);  // negated, as m
+                    T in;
+                    m = gate_split(sg, lam, in);
+                    k.store(gx + i * a.C, in);
+                    k.store(gg + i * a.C, vmul(vmul(gate_slope_neg(sg), Sp::H(p)), lam));
+                }
+        };
+        const int whole = steps / U * U;
+        for (int t0 = 0; t0 < whole; t0 += U) forward(std::true_type{}, t0, U);
+        if (whole < steps) {
+            forward(std::false_type{}, whole, steps - whole);
+            backward(std::false_type{}, whole, steps - whole);
+        }
+        for (int t0 = whole - U; t0 >= 0; t0 -= U) backward(std::true_type{}, t0, U);
+        if (a.state_out) k.store(a.state_out + k.b * a.C + k.c, neg(m));
+    }
+    grid_dep_launch_dependents();
+}
+
 // One token per row-channel: h <- f h + i x, y = h, one 16-byte vector of g per thread.  Bound by the
 // bytes of g, x, y and the state in and out: 256x32x4096 fp32 98 us, 6870 GB/s (a grid of eight
 // blocks per SM walking the rows took 114).
@@ -820,11 +938,35 @@ cudaError_t launch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t
     return ScanLaunch<TIO, V, LC, NW, ST, RES, BWD, HOW>(s)(s, a, stream);
 }
 
+// One warp per sequence and 32 V channels (backward: T <= kGatedCarrySteps).
+template <typename TIO, int V, int U, bool BWD>
+cudaError_t launch_rows(const GatedScanShape& s, ScanArgs a, cudaStream_t stream) {
+    a.groups = (s.C + 32 * V - 1) / (32 * V);
+    const int kept = BWD ? (int)s.T * 32 * (int)sizeof(typename Span<V>::P) : 0;  // bytes per warp, at most 32 KB
+    const int warps = kept > 16384 ? 1 : kept > 8192 ? 2 : 4;
+    const dim3 grid((unsigned)((s.B * a.groups + warps - 1) / warps));
+    if constexpr (BWD)
+        return launch_pdl(rows_bwd<TIO, V, U>, grid, dim3(32 * warps), warps * kept, stream, a);
+    else
+        return launch_pdl(rows_fwd<TIO, V, U>, grid, dim3(32 * warps), 0, stream, a);
+}
+
 // Times below: us on a B200 in a CUDA graph, inputs over the L2, shapes B x T x C.
 //
 // Sequences of at most kShort steps are read directly: 64x32x2048 fp32 takes 33 staged and 13 direct
 // (a short tile leaves warps idle), 32x128x2048 20 and 21, 8x1024x768 15 and 26.
 constexpr int64_t kShort = 64;
+
+// Short sequences of many channels: one warp per sequence and 32 or 64 channels instead (rows_fwd,
+// rows_bwd), at 16 warps of pairs per SM for T < 256 forward: 256x32x4096 fp32 64 against 83 direct
+// (bf16 35 against 75), 256x65x4096 129 against 286 staged (71 against 243), 40x200x4096 62 against 74
+// (42 against 63), but 40x1024x4096 326 against 315 (204 against 155).  With fewer warps single
+// channels, T < 128: 64x48x768 7.3 against 12.1, 32x128x1280 14.7 against 14.2, 16x48x1024 5.2 against
+// 4.8.  Backward, with the steps kept in shared memory: pairs for the shortest (256x8x4096 28 against
+// 34, bf16 19 against 33; 256x24x4096 58 in bf16, 92 by single channels), then single channels
+// (256x24x4096 93, 256x48x4096 197 against 279, bf16 139 against 268); fp32 not where the direct form's
+// warps come out even (256x32x4096 123 against 132, 256x64x4096 255 against 274).
+constexpr int64_t kRowsForward = 256, kRowsForwardFew = 128, kRowsBackward = kGatedCarrySteps;
 
 // Rows that TMA can stage: 4x1024x2048 forward 19, backward 33, in bf16 13 and 26.  Others are staged
 // by copies: 4x1024x2049 25, 42, 20 and 31 (direct loads took 25, 91, 46 and 71).
@@ -881,6 +1023,15 @@ cudaError_t launch_direct(const GatedScanShape& s, const ScanArgs& a, cudaStream
 template <typename TIO, bool BWD>
 cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t stream) {
     constexpr bool kHalf = sizeof(TIO) == 2;
+    const int64_t singles = s.B * ((s.C + 31) / 32), pairs = s.C % 2 == 0 ? s.B * ((s.C + 63) / 64) : 0, sms = sm_count();
+    if constexpr (BWD) {
+        if (pairs >= 16 * sms && s.T <= (kHalf ? 32 : 15)) return launch_rows<TIO, 2, 8, true>(s, a, stream);
+        if (singles >= 8 * sms && s.T > 8 && s.T <= kRowsBackward && (kHalf || s.T % 32 != 0))
+            return launch_rows<TIO, 1, 16, true>(s, a, stream);
+    } else {
+        if (pairs >= 16 * sms && s.T < kRowsForward) return launch_rows<TIO, 2, 8, false>(s, a, stream);
+        if (singles >= 5 * sms && s.T > 8 && s.T < kRowsForwardFew) return launch_rows<TIO, 1, 16, false>(s, a, stream);
+    }
     if (s.T <= kShort)
         return s.C % 2 == 0 ? launch_direct<TIO, 2, BWD>(s, a, stream) : launch_direct<TIO, 1, BWD>(s, a, stream);
     if (tma_rows(s)) {

@@ -233,13 +233,15 @@ def test_training_step_matches_oracle(shape, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(40, 700, 768), (2, 700, 4096), (1, 3000, 1000), (1, 4100, 256), (1, 4300, 33),
                                    (1, 4100, 4040), (32, 4100, 196), (2, 1000, 488), (1, 4000, 760),
-                                   (1, 4100, 257), (1, 3300, 769), (3, 1001, 257), (70, 1, 1000), (50, 3, 515), (30, 30, 1002), (20, 60, 999)],
+                                   (1, 4100, 257), (1, 3300, 769), (3, 1001, 257),
+                                   (40, 3, 3800), (40, 13, 3800), (40, 27, 3800), (40, 60, 3800), (40, 64, 3800),
+                                   (40, 130, 3800), (33, 50, 1199), (70, 1, 1000), (50, 3, 515), (30, 30, 1002), (20, 60, 999)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_training_step_configurations(shape, dtype):
     """Many channels (the time axis in one block, or few), few channels and a long axis (full clusters,
     each tile length and channels per lane), long sequences whose pairs of channels fill the device
     in clusters or in single blocks, rows that TMA cannot stage (the same splits), short sequences
-    of every length class; ragged last tiles and channel groups throughout."""
+    of every length class, of few and of many channels; ragged last tiles and channel groups throughout."""
     _check_train(dtype, *_case(*shape, seed=300 + sum(shape), dtype=dtype))
 
 
