@@ -954,8 +954,9 @@ cudaError_t launch_rows(const GatedScanShape& s, ScanArgs a, cudaStream_t stream
 // Times below: us on a B200 in a CUDA graph, inputs over the L2, shapes B x T x C.
 //
 // Sequences of at most kShort steps are read directly: 64x32x2048 fp32 takes 33 staged and 13 direct
-// (a short tile leaves warps idle), 32x128x2048 20 and 21, 8x1024x768 15 and 26.
-constexpr int64_t kShort = 64;
+// (a short tile leaves warps idle), 32x128x2048 20 and 21, 8x1024x768 15 and 26.  The bf16 backward's
+// staged tile is 64 steps: from 33 on it wins (32x48x768 7.1 against 10.5, 64x64x768 11 against 15).
+constexpr int64_t kShort = 64, kShortHalfBackward = 32;
 
 // Short sequences of many channels: one warp per sequence and 32 or 64 channels instead (rows_fwd,
 // rows_bwd), at 16 warps of pairs per SM for T < 256 forward: 256x32x4096 fp32 64 against 83 direct
@@ -964,8 +965,9 @@ constexpr int64_t kShort = 64;
 // channels, T < 128: 64x48x768 7.3 against 12.1, 32x128x1280 14.7 against 14.2, 16x48x1024 5.2 against
 // 4.8.  Backward, with the steps kept in shared memory: pairs for the shortest (256x8x4096 28 against
 // 34, bf16 19 against 33; 256x24x4096 58 in bf16, 92 by single channels), then single channels
-// (256x24x4096 93, 256x48x4096 197 against 279, bf16 139 against 268); fp32 not where the direct form's
-// warps come out even (256x32x4096 123 against 132, 256x64x4096 255 against 274).
+// (256x24x4096 93, 256x48x4096 197 against 279, bf16 139 against 268, or 169 staged); fp32 not where the
+// direct form's warps come out even (256x32x4096 123 against 132, 256x64x4096 255 against 274), bf16
+// not where tiles of 64 steps are staged nearly full (256x56x4096 173 against 222).
 constexpr int64_t kRowsForward = 256, kRowsForwardFew = 128, kRowsBackward = kGatedCarrySteps;
 
 // Rows that TMA can stage: 4x1024x2048 forward 19, backward 33, in bf16 13 and 26.  Others are staged
@@ -1023,18 +1025,20 @@ cudaError_t launch_direct(const GatedScanShape& s, const ScanArgs& a, cudaStream
 template <typename TIO, bool BWD>
 cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t stream) {
     constexpr bool kHalf = sizeof(TIO) == 2;
-    const int64_t singles = s.B * ((s.C + 31) / 32), pairs = s.C % 2 == 0 ? s.B * ((s.C + 63) / 64) : 0, sms = sm_count();
+    const bool tma = tma_rows(s);
+    const int64_t singles = s.B * ((s.C + 31) / 32), sms = sm_count();
+    const int64_t pairs = s.C % 2 == 0 ? s.B * ((s.C + 63) / 64) : 0;
     if constexpr (BWD) {
         if (pairs >= 16 * sms && s.T <= (kHalf ? 32 : 15)) return launch_rows<TIO, 2, 8, true>(s, a, stream);
-        if (singles >= 8 * sms && s.T > 8 && s.T <= kRowsBackward && (kHalf || s.T % 32 != 0))
+        if (singles >= 8 * sms && s.T > 8 && s.T <= (kHalf && tma ? 48 : kRowsBackward) && (kHalf || s.T % 32 != 0))
             return launch_rows<TIO, 1, 16, true>(s, a, stream);
     } else {
         if (pairs >= 16 * sms && s.T < kRowsForward) return launch_rows<TIO, 2, 8, false>(s, a, stream);
         if (singles >= 5 * sms && s.T > 8 && s.T < kRowsForwardFew) return launch_rows<TIO, 1, 16, false>(s, a, stream);
     }
-    if (s.T <= kShort)
+    if (s.T <= (BWD && kHalf && tma ? kShortHalfBackward : kShort))
         return s.C % 2 == 0 ? launch_direct<TIO, 2, BWD>(s, a, stream) : launch_direct<TIO, 1, BWD>(s, a, stream);
-    if (tma_rows(s)) {
+    if (tma) {
         if constexpr (!kHalf)
             if (s.T >= kLong) {
                 ScanLaunch<TIO, 2, BWD ? 16 : 32, BWD ? 8 : 4, 2, 1, BWD> pairs(s);

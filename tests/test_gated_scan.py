@@ -235,7 +235,8 @@ def test_training_step_matches_oracle(shape, dtype):
                                    (1, 4100, 4040), (32, 4100, 196), (2, 1000, 488), (1, 4000, 760),
                                    (1, 4100, 257), (1, 3300, 769), (3, 1001, 257),
                                    (40, 3, 3800), (40, 13, 3800), (40, 27, 3800), (40, 60, 3800), (40, 64, 3800),
-                                   (40, 130, 3800), (33, 50, 1199), (70, 1, 1000), (50, 3, 515), (30, 30, 1002), (20, 60, 999)],
+                                   (40, 130, 3800), (33, 50, 1199), (70, 1, 1000), (50, 3, 515), (30, 30, 1002), (20, 60, 999),
+                                   (20, 40, 1000), (20, 64, 1000), (40, 56, 3800), (40, 45, 3801)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_training_step_configurations(shape, dtype):
     """Many channels (the time axis in one block, or few), few channels and a long axis (full clusters,
