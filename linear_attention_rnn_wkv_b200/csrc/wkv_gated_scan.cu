@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(128) rows_bwd(ScanArgs a) {
     using T = typename Lanes<V>::T;
     using P = typename Span<V>::P;
     using Sp = Span<V>;
-    extern __shared__ __align__(16) unsigned char slots[];
+    extern __shared__ __align__(1024) unsigned char slots[];
     const Rows<V> k(a);
     grid_dep_wait();  // before any global memory access
     if (k.live) {
