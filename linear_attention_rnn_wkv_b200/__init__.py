@@ -103,10 +103,12 @@ def lib():
                 L.wkv_status_string.restype = ctypes.c_char_p
                 L.wkv_forward_auto_path.argtypes = [i64, i64, i64, i32]
                 L.wkv_testhook_forward_drop.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp, vp, sz, i64, u32, vp]
+                L.wkv_testhook_gated_scan_drop.argtypes = [i64, i64, i64, i32] + [vp] * 6 + [i32, i32, u32, vp]
                 for f in (L.wkv_forward, L.wkv_forward_ex, L.wkv_workspace_init, L.wkv_forward_status,
                           L.wkv_get_device_status, L.wkv_forward_gated, L.token_shift_mix3, L.wkv_backward,
                           L.wkv_decode_step, L.wkv_decode_step_fused, L.token_shift_mix,
-                          L.wkv_forward_auto_path, L.wkv_testhook_forward_drop, L.gated_scan_forward,
+                          L.wkv_forward_auto_path, L.wkv_testhook_forward_drop,
+                          L.wkv_testhook_gated_scan_drop, L.gated_scan_forward,
                           L.gated_scan_backward, L.gated_scan_step, L.group_norm_gated,
                           L.group_norm_gated_backward):
                     f.restype = i32

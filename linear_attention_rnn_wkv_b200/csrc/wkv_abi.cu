@@ -508,4 +508,22 @@ wkv_status wkv_testhook_forward_drop(int64_t B, int64_t T, int64_t C, const floa
                         0, spin_limit, drop_unit, stream);
 }
 
+// Test hook (not in wkv.h): the gated scan's forward (out0 = y) or backward (with carry and gy: out0 = gx,
+// out1 = gg), from and to no state, in which the block of rank drop_sums in each cluster withholds its sums, or
+// that of rank drop_tile the fetch of its first tile (-1: none), and every bounded wait gives up after
+// spin_limit polls.
+wkv_status wkv_testhook_gated_scan_drop(int64_t B, int64_t T, int64_t C, wkv_dtype io, const void* g, const void* x,
+                                        const float* carry, const void* gy, void* out0, void* out1, int drop_sums,
+                                        int drop_tile, uint32_t spin_limit, cudaStream_t stream) {
+    const GatedScanShape shape{B, T, C, (int)io};
+    GatedScanWaits waits;
+    waits.spin_limit = spin_limit;
+    waits.drop_sums = drop_sums;
+    waits.drop_tile = drop_tile;
+    const cudaError_t e =
+        gy ? launch_gated_scan_backward(shape, g, x, carry, gy, nullptr, out1, out0, nullptr, stream, waits)
+           : launch_gated_scan_forward(shape, g, x, nullptr, out0, nullptr, nullptr, stream, waits);
+    return e == cudaSuccess ? WKV_OK : cuda_fail(e);
+}
+
 }  // extern "C"

@@ -5,6 +5,8 @@
 
 #include <cuda_runtime.h>
 
+#include "wkv_internal.h"
+
 namespace wkvb {
 
 // Steps from one saved state to the next (the forward's `carry`, read by the backward).
@@ -18,11 +20,19 @@ struct GatedScanShape {
 // Whether one launch's grid holds the shape.
 bool gated_scan_fits(const GatedScanShape& s);
 
+// The scan's bounded waits; for tests, the rank in its cluster of a block that withholds its sums, or the
+// fetch of its first tile (-1: none).
+struct GatedScanWaits {
+    uint32_t spin_limit = kSpinLimitDefault;
+    int drop_sums = -1, drop_tile = -1;
+};
+
 cudaError_t launch_gated_scan_forward(const GatedScanShape& s, const void* g, const void* x, const float* state_in,
-                                      void* y, float* state_out, float* carry, cudaStream_t stream);
+                                      void* y, float* state_out, float* carry, cudaStream_t stream,
+                                      const GatedScanWaits& waits = {});
 cudaError_t launch_gated_scan_backward(const GatedScanShape& s, const void* g, const void* x, const float* carry,
                                        const void* gy, const float* gstate_out, void* gg, void* gx, float* gstate_in,
-                                       cudaStream_t stream);
+                                       cudaStream_t stream, const GatedScanWaits& waits = {});
 // n row-channels
 cudaError_t launch_gated_scan_step(int64_t n, int io, const void* g, const void* x, float* state, void* y,
                                    cudaStream_t s);

@@ -57,6 +57,9 @@ struct ScanArgs {
     float* carry;            // [B][saved_states(T)][C]: forward writes (or null), backward reads
     const float* gstate;     // backward: gradient of state_out, [B][C] or null
     uint32_t* dev_err;       // the library's device-wide error word
+    uint32_t spin_limit;     // bounded waits
+    int drop_sums, drop_tile; // test hook: the block of this rank withholds its sums, or the fetch of its
+                              // first tile (-1: none)
 };
 
 __device__ __forceinline__ int64_t saved_states(int64_t T) { return (T + kGatedCarrySteps - 1) / kGatedCarrySteps; }
@@ -204,6 +207,11 @@ struct Tile {
 template <typename TIO, How HOW>
 constexpr bool stages_gy_apart = HOW == kTma && sizeof(TIO) == 2;
 
+// Waits, with a limit, for the end of a mbarrier's phase, whichever it is; runs out where none is under way.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t limit) {
+    for (uint32_t parity = 0; parity < 2; ++parity) mbar_wait(bar, parity, limit);
+}
+
 // A ring of ST staged tiles, completion on the slot's barrier.  A slot is refilled right after the
 // block's barrier behind which every lane has its values in registers: by thread 0 (TMA), or by all
 // threads (copies).
@@ -246,7 +254,16 @@ struct Ring {
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[slot])) : "memory");
         }
     }
-    __device__ __forceinline__ bool wait(int it) { return mbar_wait(&full[it % ST], (it / ST) & 1, kSpinLimitDefault); }
+    __device__ __forceinline__ bool wait(int it, uint32_t limit) {
+        uint64_t* b = &full[it % ST];
+        const uint32_t p = (it / ST) & 1;
+        return mbar_try_wait_hint(b, p, kWaitHintNs) || mbar_wait(b, p, limit);
+    }
+    // every copy under way has landed, or its wait runs out
+    __device__ __forceinline__ void drain(uint32_t limit) {
+        if (HOW == kCopy) asm volatile("cp.async.wait_all;" ::: "memory");
+        for (int i = 0; i < ST; ++i) mbar_drain(&full[i], limit);
+    }
     // this lane's channels of row r of array k; `element`: the row's first element within the
     // arrays, modulo 2^32
     __device__ __forceinline__ typename Lanes<V>::T get(int it, int k, int r, uint32_t element) const {
@@ -299,7 +316,14 @@ struct Exchange {
                      "f"(p.x), "f"(p.y), "f"(p.z), "f"(p.w), "r"(on)
                      : "memory");
     }
-    __device__ __forceinline__ bool wait(int it) { return mbar_wait(&bar[it & 1], (it >> 1) & 1, kSpinLimitDefault); }
+    __device__ __forceinline__ bool wait(int it, uint32_t limit) {
+        return mbar_wait(&bar[it & 1], (it >> 1) & 1, limit);
+    }
+    // what the others have sent has landed, or the waits run out
+    __device__ __forceinline__ void drain(uint32_t limit) {
+        mbar_drain(&bar[0], limit);
+        mbar_drain(&bar[1], limit);
+    }
 };
 
 // (A as a signed gate, H) of a span, V channels, as one vector
@@ -381,7 +405,16 @@ struct Block {
     __device__ __forceinline__ void store_state(float* p, int64_t row, T v) const {
         if (p) store(p + row * a.C + c, v, false);
     }
-    __device__ __forceinline__ void gave_up() const {
+    // Polls of this thread's bounded waits; 0 once one has run out.  It then fetches, expects and sends
+    // nothing: no slot is filled and no phase of a mbarrier begun while the last is under way, since each is
+    // begun by a thread that has seen the last one end.  Threads that then miss it run out in turn, once
+    // each, the walk goes on to its end without waiting, and the block stays until what may still be
+    // under way to it has landed (drain).
+    uint32_t limit = a.spin_limit;
+    __device__ __forceinline__ bool well() const { return limit != 0; }
+    __device__ __forceinline__ void got(bool ok) {
+        if (ok) return;
+        limit = 0;
         atomicCAS(a.dev_err, kDevOk, (uint32_t)kDevTimeoutCopy);
     }
 };
@@ -397,7 +430,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
     __shared__ P wsum[2][NW][32];  // the warps' (s, H)
     __shared__ P csum[2][kMaxCluster][32];
     __shared__ uint64_t bars[(ST ? ST : 1) + 2];
-    const B k(a);
+    B k(a);
     Ring<TIO, V, LC * NW, 32 * NW, 2, ST ? ST : 1, HOW> ring{slots, bars + 2, k.c - k.cl, k.b, a.T, a.C,
                                                              a.B * a.T * a.C * (int64_t)sizeof(TIO)};
     Exchange<P> ex{csum, bars};
@@ -418,7 +451,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
     grid_dep_wait();  // before any global memory access
     if (ST && ring.mine())
         for (int it = 0; it < ST && (int64_t)it * S + rank < tiles; ++it)
-            ring.fetch(it, (it * (int64_t)S + rank) * k.tile, maps, from);
+            if (it || (int)rank != a.drop_tile) ring.fetch(it, (it * (int64_t)S + rank) * k.tile, maps, from);
     T carry = k.load_state(a.state_in, k.b);
     if (S > 1) {
         cluster_wait();  // every block of the cluster runs and its barriers are ready
@@ -461,9 +494,9 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
         }
         P(*ws)[32] = wsum[it & 1];
         ws[k.warp][k.lane] = Sp::pack(B::seal(A, Dn), H);
-        if (S > 1 && threadIdx.x == 0) ex.expect(it, S);
+        if (S > 1 && threadIdx.x == 0 && k.well()) ex.expect(it, S);
         __syncthreads();
-        if (ST && ring.mine() && j + (int64_t)ST * S < tiles)
+        if (ST && ring.mine() && k.well() && j + (int64_t)ST * S < tiles)
             ring.fetch(it + ST, (j + (int64_t)ST * S) * k.tile, maps, from);
         // this warp's channels: warps w0 .. w0 + WT - 1 in time order
         const int w0 = ST ? 0 : k.warp - k.wt, WT = ST ? NW : k.WT;
@@ -483,9 +516,9 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
             const T ps = span_gate(tA, tD), pH = tH;
             if (k.wt == NW - 1) {
                 fold(NW - 1);
-                ex.send(it, S, rank, k.lane, Sp::pack(span_gate(tA, tD), tH));
+                if (k.well() && (int)rank != a.drop_sums) ex.send(it, S, rank, k.lane, Sp::pack(span_gate(tA, tD), tH));
             }
-            if (!ex.wait(it) && k.lane == 0) k.gave_up();
+            k.got(ex.wait(it, k.limit));
             for (uint32_t r = 0; r < S; ++r) {
                 if (r == rank) h = carry;
                 const P p = csum[it & 1][r][k.lane];
@@ -513,17 +546,19 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_fwd(ScanArgs a, const __gr
         // kernel is this one again (bf16 backward, 4x1024x4096: 37 against 45 us)
         if (j0 + S >= tiles) grid_dep_launch_dependents();
         const int64_t j = j0 + rank, t0 = j * k.tile + k.wt * LC;
-        if (ST && j < tiles && !ring.wait(it) && k.lane == 0) k.gave_up();
+        if (ST && j < tiles) k.got(ring.wait(it, k.limit));
         if (k.whole && (j + 1) * k.tile <= a.T)  // the same for every warp of the block
             stride(std::true_type{}, j, t0, LC);
         else
             stride(std::false_type{}, j, t0, t0 < a.T ? (int)min64(LC, a.T - t0) : 0);
     }
+    if (ST && !k.well() && ring.mine()) ring.drain(a.spin_limit);
     if (rank == 0 && k.wt == 0) k.store_state(a.state_out, k.b, carry);
     if (S > 1) {  // no block leaves while another may still send to it
         __syncwarp();
         cluster_arrive_relaxed();
         cluster_wait();
+        if (!k.well()) ex.drain(a.spin_limit);
     }
 }
 
@@ -551,7 +586,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
     __shared__ T wadj[2][NW][32];  // and M
     __shared__ P csum[2][kMaxCluster][32];
     __shared__ uint64_t bars[2 + kST + (kLate ? kST + 1 : 0)];
-    const B k(a);
+    B k(a);
     const int64_t bytes = a.B * a.T * a.C * (int64_t)sizeof(TIO);
     Ring<TIO, V, LC * NW, 32 * NW, kEarly, kST, HOW> ring{slots, bars + 2, k.c - k.cl, k.b, a.T, a.C, bytes};
     Ring<TIO, V, LC * NW, 32 * NW, 1, kST + 1, HOW> late{slots + ST * kEarly * Tile<TIO, V, LC * NW, HOW>::kBytes,
@@ -579,7 +614,8 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         if (kLate) late.fetch(it, j * k.tile, maps + 2, from + 2);
     };
     if (ST && ring.mine())
-        for (int it = 0; it < ST; ++it) fetch(it, tiles - 1 - it * (int64_t)S - rank);
+        for (int it = 0; it < ST; ++it)
+            if (it || (int)rank != a.drop_tile) fetch(it, tiles - 1 - it * (int64_t)S - rank);
     T carry = neg(k.load_state(a.gstate, k.b));
     const int64_t states0 = k.b * saved_states(a.T);
     if (S > 1) {
@@ -635,7 +671,7 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
             H = vfma(sg[s], d, pick(sg[s], H, x[s]));
             x[s] = d;
         }
-        if (kLate && j >= 0 && !late.wait(it) && k.lane == 0) k.gave_up();
+        if (kLate && j >= 0) k.got(late.wait(it, k.limit));
 #pragma unroll
         for (int s = LC - 1; s >= 0; --s) {
             M = gate_decay(sg[s], vsub(M, gy_at(s)));
@@ -645,9 +681,9 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         T(*wm)[32] = wadj[it & 1];
         ws[k.warp][k.lane] = Sp::pack(B::seal(A, Dn), H);
         wm[k.warp][k.lane] = M;
-        if (S > 1 && threadIdx.x == 0) ex.expect(it, S);
+        if (S > 1 && threadIdx.x == 0 && k.well()) ex.expect(it, S);
         __syncthreads();
-        if (ST && ring.mine()) fetch(it + ST, j - (int64_t)ST * S);  // gy's slot is the stride's before
+        if (ST && ring.mine() && k.well()) fetch(it + ST, j - (int64_t)ST * S);  // gy's slot is the stride's before
         const int w0 = ST ? 0 : k.warp - k.wt, WT = ST ? NW : k.WT;
 #pragma unroll
         for (int w = 0; w < WT - 1; ++w)
@@ -669,8 +705,8 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
                 tA = span_decay(sw, tA);
                 tM = span_step(sw, wm[w][k.lane], tM);
             }
-            if (k.wt == 0) ex.send(it, S, rank, k.lane, Sp::pack(span_gate(tA, tD), tM));
-            if (!ex.wait(it) && k.lane == 0) k.gave_up();
+            if (k.wt == 0 && k.well() && (int)rank != a.drop_sums) ex.send(it, S, rank, k.lane, Sp::pack(span_gate(tA, tD), tM));
+            k.got(ex.wait(it, k.limit));
             for (uint32_t r = 0; r < S; ++r) {
                 if (r == rank) m = carry;
                 const P p = csum[it & 1][r][k.lane];
@@ -701,17 +737,22 @@ __global__ void __launch_bounds__(32 * NW, MINB) scan_bwd(ScanArgs a, const __gr
         if (j0 + S >= tiles) grid_dep_launch_dependents();  // not sooner, as in the forward
         const int64_t j = tiles - 1 - j0 - rank;  // < 0: past the sequence's start
         const int64_t t0 = j * k.tile + k.wt * LC;
-        if (ST && j >= 0 && !ring.wait(it) && k.lane == 0) k.gave_up();
+        if (ST && j >= 0) k.got(ring.wait(it, k.limit));
         if (k.whole && j >= 0 && (j + 1) * k.tile <= a.T)
             stride(std::true_type{}, j, t0, LC);
         else
             stride(std::false_type{}, j, t0, j >= 0 && t0 < a.T ? (int)min64(LC, a.T - t0) : 0);
+    }
+    if (ST && !k.well() && ring.mine()) {
+        ring.drain(a.spin_limit);
+        if (kLate) late.drain(a.spin_limit);
     }
     if (rank == 0 && k.wt == 0) k.store_state(a.state_out, k.b, neg(carry));
     if (S > 1) {
         __syncwarp();
         cluster_arrive_relaxed();
         cluster_wait();
+        if (!k.well()) ex.drain(a.spin_limit);
     }
 }
 
@@ -906,7 +947,9 @@ struct ClusterRoom {
 template <typename TIO, int V, int LC, int NW, int ST, int RES, bool BWD, How HOW = kTma>
 struct ScanLaunch {
     static constexpr int kArrays = BWD ? 3 : 2;
-    static constexpr int kSmem = (ST * kArrays + (BWD && stages_gy_apart<TIO, HOW>)) * Tile<TIO, V, LC * NW, HOW>::kBytes;
+    static constexpr int kTiles = (ST * kArrays + (BWD && stages_gy_apart<TIO, HOW>)) * Tile<TIO, V, LC * NW, HOW>::kBytes;
+    // one block per SM where the rules below count on it, however few registers it takes
+    static constexpr int kSmem = RES == 1 && kTiles < 116 * 1024 ? 116 * 1024 : kTiles;
     static_assert((ST > 0) == (HOW != kDirect), "direct loads stage nothing");
 
     int wt_log = 0, S = 0;  // log2 of the warps along time, blocks per cluster
@@ -1139,7 +1182,8 @@ bool gated_scan_fits(const GatedScanShape& s) {
 }
 
 cudaError_t launch_gated_scan_forward(const GatedScanShape& s, const void* g, const void* x, const float* state_in,
-                                      void* y, float* state_out, float* carry, cudaStream_t stream) {
+                                      void* y, float* state_out, float* carry, cudaStream_t stream,
+                                      const GatedScanWaits& waits) {
     if (s.T == 0)
         return state_out ? launch_pdl(copy_or_zero, dim3(flat_blocks(s.B * s.C)), dim3(256), 0, stream, s.B * s.C,
                                       state_in, state_out)
@@ -1156,12 +1200,15 @@ cudaError_t launch_gated_scan_forward(const GatedScanShape& s, const void* g, co
     a.carry = carry;
     a.dev_err = device_status_word();
     if (!a.dev_err) return cudaGetLastError();
+    a.spin_limit = waits.spin_limit;
+    a.drop_sums = waits.drop_sums;
+    a.drop_tile = waits.drop_tile;
     return s.io == 1 ? dispatch_scan<__nv_bfloat16, false>(s, a, stream) : dispatch_scan<float, false>(s, a, stream);
 }
 
 cudaError_t launch_gated_scan_backward(const GatedScanShape& s, const void* g, const void* x, const float* carry,
                                        const void* gy, const float* gstate_out, void* gg, void* gx, float* gstate_in,
-                                       cudaStream_t stream) {
+                                       cudaStream_t stream, const GatedScanWaits& waits) {
     if (s.T == 0)
         return gstate_in ? launch_pdl(copy_or_zero, dim3(flat_blocks(s.B * s.C)), dim3(256), 0, stream, s.B * s.C,
                                       gstate_out, gstate_in)
@@ -1180,6 +1227,9 @@ cudaError_t launch_gated_scan_backward(const GatedScanShape& s, const void* g, c
     a.carry = const_cast<float*>(carry);
     a.dev_err = device_status_word();
     if (!a.dev_err) return cudaGetLastError();
+    a.spin_limit = waits.spin_limit;
+    a.drop_sums = waits.drop_sums;
+    a.drop_tile = waits.drop_tile;
     return s.io == 1 ? dispatch_scan<__nv_bfloat16, true>(s, a, stream) : dispatch_scan<float, true>(s, a, stream);
 }
 
