@@ -1015,12 +1015,16 @@ cudaError_t launch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream_t
     return ScanLaunch<TIO, V, LC, NW, ST, RES, BWD, HOW>(s)(s, a, stream);
 }
 
+// Bytes of the steps that a warp of rows_bwd keeps in shared memory, at the most: two such warps, or four of
+// half, take 32 KB, which a block has without asking.
+constexpr int kRowsKept = 16384;
+
 // One warp per sequence and 32 V channels (backward: T <= kGatedCarrySteps).
 template <typename TIO, int V, int U, bool BWD>
 cudaError_t launch_rows(const GatedScanShape& s, ScanArgs a, cudaStream_t stream) {
     a.groups = (s.C + 32 * V - 1) / (32 * V);
-    const int kept = BWD ? (int)s.T * 32 * (int)sizeof(typename Span<V>::P) : 0;  // bytes per warp, at most 32 KB
-    const int warps = kept > 16384 ? 1 : kept > 8192 ? 2 : 4;
+    const int kept = BWD ? (int)s.T * 32 * (int)sizeof(typename Span<V>::P) : 0;  // bytes per warp
+    const int warps = kept > kRowsKept / 2 ? 2 : 4;
     const dim3 grid((unsigned)((s.B * a.groups + warps - 1) / warps));
     if constexpr (BWD)
         return launch_pdl(rows_bwd<TIO, V, U>, grid, dim3(32 * warps), warps * kept, stream, a);
@@ -1106,7 +1110,10 @@ cudaError_t dispatch_scan(const GatedScanShape& s, const ScanArgs& a, cudaStream
     const int64_t singles = s.B * ((s.C + 31) / 32), sms = sm_count();
     const int64_t pairs = s.C % 2 == 0 ? s.B * ((s.C + 63) / 64) : 0;
     if constexpr (BWD) {
-        if (pairs >= 16 * sms && s.T <= (kHalf ? 32 : 15)) return launch_rows<TIO, 2, 8, true>(s, a, stream);
+        constexpr int64_t kPairs = kHalf ? 32 : 15;
+        static_assert(kPairs * 32 * sizeof(Span<2>::P) <= kRowsKept && kRowsBackward * 32 * sizeof(Span<1>::P) <= kRowsKept,
+                      "launch_rows has two warps to a block at the least");
+        if (pairs >= 16 * sms && s.T <= kPairs) return launch_rows<TIO, 2, 8, true>(s, a, stream);
         if (singles >= 8 * sms && s.T > 8 && s.T <= (kHalf && tma ? 48 : kRowsBackward) && (kHalf || s.T % 32 != 0))
             return launch_rows<TIO, 1, 16, true>(s, a, stream);
     } else {

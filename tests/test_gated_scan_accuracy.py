@@ -177,3 +177,12 @@ def test_gate_ranges_within_the_recurrences_own_bound(shape, g_mean, g_std, dtyp
     """Half-open gates, gates that hold for thousands of tokens, gates that forget at once, both ends
     mixed, and gates that mostly remember."""
     _run(dtype, _random(*shape, g_mean, g_std, seed=700, dtype=dtype))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,dtype", [((40, 15, 3800), "f32"), ((40, 32, 3800), "bf16"), ((40, 63, 3801), "f32"),
+                                         ((40, 64, 3801), "bf16"), ((40, 48, 3800), "bf16")],
+                         ids=lambda v: v if isinstance(v, str) else "x".join(map(str, v)))
+def test_longest_sequences_walked_from_shared_memory(shape, dtype):
+    """The backward that keeps a warp's steps in shared memory, at the most steps of each of its forms."""
+    _run(dtype, _random(*shape, 2.0, 1.5, seed=710, dtype=dtype))
