@@ -186,3 +186,29 @@ def test_gate_ranges_within_the_recurrences_own_bound(shape, g_mean, g_std, dtyp
 def test_longest_sequences_walked_from_shared_memory(shape, dtype):
     """The backward that keeps a warp's steps in shared memory, at the most steps of each of its forms."""
     _run(dtype, _random(*shape, 2.0, 1.5, seed=710, dtype=dtype))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [4096, 4097])
+def test_both_ends_of_a_sequence_beyond_32_bit_offsets(C):
+    """More than 2^31 elements: the last 256 tokens, from the state saved before them, and the first 256, whose
+    adjoint a closed gate at the 257th cuts off from the rest, against the fp64 recurrence element by element."""
+    import torch
+    import linear_attention_rnn_wkv_b200 as wkv
+    T, n = 64 * 8300, 256
+    assert T * C > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(720)
+    r = lambda: torch.empty(1, T, C, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    g, x, gy = r(), r(), r()
+    g[:, n] = -torch.inf
+    y, so, carry = wkv.gated_scan_forward(g, x, want_carry=True)
+    gg, gx, gsi = wkv.gated_scan_backward(g, x, carry, gy)
+    assert not gg[:, n].any() and torch.equal(y[:, n], x[:, n])
+    zeros = np.zeros((1, C), np.float32)
+    up = lambda *a: [t.float().cpu().numpy() for t in a]
+    for at, s0, ends in ((0, zeros, dict(gstate_in=gsi)), (T - n, up(carry[:, (T - n) // 64])[0], dict(state_out=so))):
+        span = slice(at, at + n)
+        case = up(g[:, span], x[:, span], gy[:, span])
+        val, bound = _exact(case[0], case[1], s0, case[2], zeros)
+        _check(dict(y=y[:, span], gg=gg[:, span], gx=gx[:, span], carry=carry[:, at // 64:at // 64 + n // 64], **ends),
+               val, bound, "bf16")
