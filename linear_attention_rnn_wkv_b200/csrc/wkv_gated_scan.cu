@@ -49,6 +49,8 @@ struct ScanArgs {
     int64_t B, T, C;
     int64_t groups;  // channel groups per sequence
     int wt_log;      // log2 of the warps of a block along time (NW unless a shorter tile holds T)
+    int16_t drop_sums, drop_tile;  // test hook: the block of this rank withholds its sums, or the fetch of its
+                                   // first tile (-1: none)
     const void *g, *x, *gy;
     const float* state_in;   // forward: [B][C] or null
     void* y;                 // forward: y; backward: gx
@@ -58,9 +60,10 @@ struct ScanArgs {
     const float* gstate;     // backward: gradient of state_out, [B][C] or null
     uint32_t* dev_err;       // the library's device-wide error word
     uint32_t spin_limit;     // bounded waits
-    int drop_sums, drop_tile; // test hook: the block of this rank withholds its sums, or the fetch of its
-                              // first tile (-1: none)
 };
+// The kernels' tensor maps, 128 bytes each, follow it.  Where they straddle two lines of 128 bytes the bf16
+// forward is 4 to 6% slower (64x1024x768 53 -> 56).
+static_assert(sizeof(ScanArgs) == 128);
 
 __device__ __forceinline__ int64_t saved_states(int64_t T) { return (T + kGatedCarrySteps - 1) / kGatedCarrySteps; }
 
@@ -151,9 +154,9 @@ __device__ __forceinline__ T gate_split(T s, T a, T& input_neg) {
 // sum of -i_t A_{t-1} (one fused multiply-add of s and A per step; right while every step holds, and
 // A > 1/2 means that every one did).  The product alone, near 1, rounds the same way in span after span:
 // with steady gates of logit 9 to 17 (1x16384x64) the final state was off by up to 7600 units of 2^-24 of
-// its scale, and is by at most 30 in this form.  It costs up to 4% forward and 8% backward (4x4096x2048
-// bf16 39 and 80 us, 8x1024x768 fp32 15.5 and 26).  Dn starts below zero, so that the sign is there from
-// the start.
+// its scale, and is by at most 30 in this form.  It costs 0 to 4% forward and 0 to 7% backward (8x1024x768
+// fp32 15.5 and 26.1 us, as before; 4x4096x2048 bf16 39 and 78 against 39 and 75).  Dn starts below zero, so
+// that the sign is there from the start.
 constexpr float kNoDecay = -1.17549435e-38f;
 __device__ __forceinline__ float span_gate(float A, float Dn) { return A > 0.5f ? Dn : A; }
 __device__ __forceinline__ float2 span_gate(float2 A, float2 Dn) {
@@ -1208,8 +1211,8 @@ cudaError_t launch_gated_scan_forward(const GatedScanShape& s, const void* g, co
     a.dev_err = device_status_word();
     if (!a.dev_err) return cudaGetLastError();
     a.spin_limit = waits.spin_limit;
-    a.drop_sums = waits.drop_sums;
-    a.drop_tile = waits.drop_tile;
+    a.drop_sums = (int16_t)waits.drop_sums;
+    a.drop_tile = (int16_t)waits.drop_tile;
     return s.io == 1 ? dispatch_scan<__nv_bfloat16, false>(s, a, stream) : dispatch_scan<float, false>(s, a, stream);
 }
 
@@ -1235,8 +1238,8 @@ cudaError_t launch_gated_scan_backward(const GatedScanShape& s, const void* g, c
     a.dev_err = device_status_word();
     if (!a.dev_err) return cudaGetLastError();
     a.spin_limit = waits.spin_limit;
-    a.drop_sums = waits.drop_sums;
-    a.drop_tile = waits.drop_tile;
+    a.drop_sums = (int16_t)waits.drop_sums;
+    a.drop_tile = (int16_t)waits.drop_tile;
     return s.io == 1 ? dispatch_scan<__nv_bfloat16, true>(s, a, stream) : dispatch_scan<float, true>(s, a, stream);
 }
 
