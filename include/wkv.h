@@ -335,8 +335,9 @@ wkv_status eagle_decode_step(int64_t N, int64_t L, int64_t C, const float* w, co
  *
  * g is the gate's logit: g = +inf keeps the state to its rounding whatever the finite x (a
  * padding token), g = -inf replaces it (h_t = x_t exactly: a document boundary).  A state buffer is
- * [rows][C] fp32, the empty state zeros.  Arithmetic is fp32 for both I/O types; x and states
- * may reach 2^126 in magnitude (their differences are taken).  A NaN gate, or a non-finite x or
+ * [rows][C] fp32, the empty state zeros.  Arithmetic is fp32 for both I/O types, and a state is
+ * rounded once or twice per token up to 256 tokens, once per 16 tokens or fewer times beyond; x and
+ * states may reach 2^126 in magnitude (their differences are taken).  A NaN gate, or a non-finite x or
  * state, makes the later outputs of its sequence and channel non-finite and touches no other
  * channel.
  *

@@ -14,11 +14,11 @@
 // channels enough for every warp, nothing is split: a warp walks its channels' whole sequence.
 //
 // Bound by HBM: g and x are read once, y written once.  B200, forward (backward) against the
-// copy rate of 6549 GB/s: 1x16384x4096 fp32 118 us, 6830 GB/s (213 us, 6300 GB/s); 4x4096x2048
-// bf16 38.5 us, 5230 GB/s (74.6 us, 4500 GB/s); 64x1024x768 bf16 52.6 us, 5740 GB/s (91.4 us, 5510
-// GB/s); 8x1024x768 fp32 15.0 us, 5040 GB/s (25.3 us, 4970 GB/s).  In bf16 a byte carries twice the
-// tokens and instructions are the limit (18 per token forward, 42 backward, at half of the issue
-// slots or a little more: two or three warps per scheduler).
+// copy rate of 6549 GB/s: 1x16384x4096 fp32 119 us, 6770 GB/s (220 us, 6100 GB/s); 4x4096x2048
+// bf16 39.5 us, 5100 GB/s (78.2 us, 4290 GB/s); 64x1024x768 bf16 53.8 us, 5610 GB/s (93.0 us, 5410
+// GB/s); 8x1024x768 fp32 15.5 us, 4870 GB/s (26.1 us, 4820 GB/s).  In bf16 a byte carries twice the
+// tokens and the warps issue 19 instructions per token forward, 44 backward, in 52 and 60% of the issue
+// slots: two or three warps per scheduler, which wait for fixed latencies in between.
 //
 // Arithmetic: fp32 whatever the I/O type.  A gate is kept as the smaller of (f, i) with a sign,
 // from e = 2^(-|g| log2 e) as e / (1 + e), relatively accurate at both ends.  A step starts from
@@ -1035,7 +1035,9 @@ cudaError_t launch_rows(const GatedScanShape& s, ScanArgs a, cudaStream_t stream
         return launch_pdl(rows_fwd<TIO, V, U>, grid, dim3(32 * warps), 0, stream, a);
 }
 
-// Times below: us on a B200 in a CUDA graph, inputs over the L2, shapes B x T x C.
+// Times below: us on a B200 in a CUDA graph, inputs over the L2, shapes B x T x C.  Those of staged forms were
+// taken before spans carried 1 - A (span_gate): both sides of a comparison are up to 4% (forward) and 7%
+// (backward) slower since.
 //
 // Sequences of at most kShort steps are read directly: 64x32x2048 fp32 takes 33 staged and 13 direct
 // (a short tile leaves warps idle), 32x128x2048 20 and 21, 8x1024x768 15 and 26.  The bf16 backward's
@@ -1049,9 +1051,10 @@ constexpr int64_t kShort = 64, kShortHalfBackward = 32;
 // channels, T < 128: 64x48x768 7.3 against 12.1, 32x128x1280 14.7 against 14.2, 16x48x1024 5.2 against
 // 4.8.  Backward, with the steps kept in shared memory: pairs for the shortest (256x8x4096 28 against
 // 34, bf16 19 against 33; 256x24x4096 58 in bf16, 92 by single channels), then single channels
-// (256x24x4096 93, 256x48x4096 197 against 279, bf16 139 against 268, or 169 staged); fp32 not where the
-// direct form's warps come out even (256x32x4096 123 against 132, 256x64x4096 255 against 274), bf16
-// not where tiles of 64 steps are staged nearly full (256x56x4096 173 against 222).
+// (256x24x4096 93, 256x48x4096 197 against 279, bf16 139 against 268, or 169 staged); fp32 not at 32 and 64
+// steps, where the direct form is the faster (256x32x4096 123 against 132, 256x64x4096 255 against 274;
+// at 16 it is not, 65 against 56), bf16 not where tiles of 64 steps are staged nearly full (256x56x4096
+// 173 against 222).
 constexpr int64_t kRowsForward = 256, kRowsForwardFew = 128, kRowsBackward = kGatedCarrySteps;
 
 // Rows that TMA can stage: 4x1024x2048 forward 19, backward 33, in bf16 13 and 26.  Others are staged
